@@ -1,6 +1,7 @@
 """MXFP4 quantize and block-scaled GEMM on AMD gfx950 (MI355X).
 
-A thin binding over the C ABI of libmxfp4.so (include/mxfp4.h). Every step
+A thin binding over the C ABI of libmxfp4.so (include/mxfp4.h and, for the
+few-token operators, include/mxfp4_fewtoken.h). Every step
 of the computation runs in the library's HIP kernels; this module only
 marshals arguments. PyTorch supplies device memory and streams.
 
@@ -9,14 +10,16 @@ Two layers, same names as the C ABI:
     mxfp4_quantize_2d, mxfp4_quantize_sr, mxfp4_quantize_2d_sr,
     mxfp4_quantize_sr_rows, mxfp4_quantize_2d_sr_rows, mxfp4_gemm,
     mxfp4_gemm_tile, mxfp4_gemm_swiglu, mxfp4_shuffle_b(_sizes), mxfp4_gemm_bshuffled,
-    mxfp4_quantize_frag, mxfp4_to_frag, mxfp4_gemm_frag take raw device
+    mxfp4_quantize_frag, mxfp4_to_frag, mxfp4_gemm_frag, mxfp4_gemv,
+    mxfp4_moe_route(_workspace), mxfp4_moe(_workspace) take raw device
     pointers (ints) and return the C status code.
   * quantize(x), quantize_2d(x), quantize_sr(x, seed, row0=0),
     quantize_2d_sr(x, seed, row0=0), gemm(...), gemm_tile(...) and
     gemm_swiglu(...) take torch tensors,
     check their dtype, device, shape and contiguity, allocate outputs when none
     are given, enqueue on torch's current stream and raise Mxfp4Error on a
-    non-zero status.
+    non-zero status. gemv(...), moe_route(...) and moe(...) do the same for a
+    few BF16 rows against MXFP4 weights (a decode step).
 
 If the library is missing the functions raise: there is no fallback path.
 """
@@ -34,6 +37,8 @@ __all__ = [
     "gemm_swiglu", "mxfp4_shuffle_b_sizes", "mxfp4_shuffle_b", "mxfp4_gemm_bshuffled",
     "shuffle_b", "gemm_bshuffled", "mxfp4_quantize_frag", "mxfp4_to_frag", "mxfp4_gemm_frag",
     "quantize_frag", "to_frag", "gemm_frag",
+    "mxfp4_gemv", "mxfp4_moe_route_workspace", "mxfp4_moe_route", "mxfp4_moe_workspace",
+    "mxfp4_moe", "gemv", "moe_route_workspace", "moe_route", "moe_workspace", "moe",
 ]
 
 OUT_BF16 = 0
@@ -96,6 +101,18 @@ def load_library():
         lib.mxfp4_to_frag.restype = i32
         lib.mxfp4_gemm_frag.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, vp]
         lib.mxfp4_gemm_frag.restype = i32
+        pi64 = ctypes.POINTER(i64)
+        lib.mxfp4_gemv.argtypes = [vp, i64, vp, vp, i64, i64, i64, i32, vp, vp]
+        lib.mxfp4_gemv.restype = i32
+        lib.mxfp4_moe_route_workspace.argtypes = [i64, i64, pi64]
+        lib.mxfp4_moe_route_workspace.restype = i32
+        lib.mxfp4_moe_route.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp]
+        lib.mxfp4_moe_route.restype = i32
+        lib.mxfp4_moe_workspace.argtypes = [i64, i64, i64, pi64]
+        lib.mxfp4_moe_workspace.restype = i32
+        lib.mxfp4_moe.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32,
+                                  vp, vp, vp]
+        lib.mxfp4_moe.restype = i32
         _lib = lib
     return _lib
 
@@ -188,6 +205,38 @@ def mxfp4_to_frag(codes, scales, R, K, codes_frag, scales_frag, stream):
 def mxfp4_gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype, C, stream):
     return int(load_library().mxfp4_gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N,
                                               K, out_dtype, C, stream))
+
+
+def mxfp4_gemv(x_bf16, ldx, W_codes, W_scales, M, N, K, out_dtype, y, stream):
+    return int(load_library().mxfp4_gemv(x_bf16, ldx, W_codes, W_scales, M, N, K, out_dtype, y,
+                                         stream))
+
+
+def mxfp4_moe_route_workspace(T, E):
+    """(rc, bytes) of moe_route's workspace."""
+    n = ctypes.c_int64(0)
+    rc = int(load_library().mxfp4_moe_route_workspace(T, E, ctypes.byref(n)))
+    return rc, n.value
+
+
+def mxfp4_moe_route(x_bf16, ldx, router_bf16, T, H, E, top_k, renormalize, ids, weights,
+                    workspace, stream):
+    return int(load_library().mxfp4_moe_route(x_bf16, ldx, router_bf16, T, H, E, top_k,
+                                              renormalize, ids, weights, workspace, stream))
+
+
+def mxfp4_moe_workspace(T, I, top_k):
+    """(rc, bytes) of moe's workspace."""
+    n = ctypes.c_int64(0)
+    rc = int(load_library().mxfp4_moe_workspace(T, I, top_k, ctypes.byref(n)))
+    return rc, n.value
+
+
+def mxfp4_moe(x_bf16, ldx, ids, weights, W13_codes, W13_scales, W2_codes, W2_scales, T, H, I, E,
+              top_k, out_dtype, y, workspace, stream):
+    return int(load_library().mxfp4_moe(x_bf16, ldx, ids, weights, W13_codes, W13_scales,
+                                        W2_codes, W2_scales, T, H, I, E, top_k, out_dtype, y,
+                                        workspace, stream))
 
 
 # ------------------------------------------------------- torch tensor layer
@@ -494,4 +543,192 @@ def gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype=N
                          _stream_handle(stream))
     if rc != 0:
         raise Mxfp4Error(rc, "mxfp4_gemm_frag")
+    return out
+
+
+# ------------------------------------------------ few-token tensor helpers
+# Called once per layer and token, where the host's time counts: one pass
+# over the arguments and no repeated look-ups.
+def _rows(x, name):
+    """(rows, cols, ldx, device index) of a 2-D BF16 tensor on the current
+    device whose rows are each contiguous, ldx elements apart (a slice of a
+    larger activation)."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device")
+    rows, cols = x.shape
+    ldx, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return rows, cols, ldx, dev
+
+
+def _check_on(t, name, dtype, shape, dev):
+    _check(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device")
+
+
+def _out_code(out_dtype, out):
+    """(torch dtype, C ABI code) of an output from out_dtype and out."""
+    import torch
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype == torch.bfloat16:
+        return out_dtype, OUT_BF16
+    if out_dtype == torch.float32:
+        return out_dtype, OUT_FP32
+    raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor whose memory torch does not hand out again before `stream`
+    (None: the current one, in whose order torch works anyway) has used it."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _scratch(nbytes, workspace, device, stream):
+    """A workspace of at least nbytes: the caller's, or a new one."""
+    import torch
+    if workspace is None:
+        workspace = _new(nbytes, torch.uint8, device, stream)
+    else:
+        _check_on(workspace, "workspace", torch.uint8, workspace.shape, device.index)
+        if workspace.numel() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
+    return workspace
+
+
+def gemv(x, codes, scales, out_dtype=None, out=None, stream=None):
+    """y[M, N] = x @ dq(W)^T for a few BF16 rows x [M, K] (rows contiguous,
+    row stride a multiple of 8) and an MXFP4 weight as quantize writes it
+    (codes [N, K/2], scales [N, K/32]); any M and N, K % 32 == 0.
+
+    out_dtype: torch.bfloat16 (default) or torch.float32.
+    """
+    import torch
+    M, K, ldx, dev = _rows(x, "x")
+    if codes.dim() != 2:
+        raise ValueError("codes must be 2-D [N, K/2]")
+    N = codes.shape[0]
+    _check_on(codes, "codes", torch.uint8, (N, K // 2), dev)
+    _check_on(scales, "scales", torch.uint8, (N, K // 32), dev)
+    out_dtype, code = _out_code(out_dtype, out)
+    if out is None:
+        out = _new((M, N), out_dtype, x.device, stream)
+    else:
+        _check_on(out, "out", out_dtype, (M, N), dev)
+    rc = mxfp4_gemv(x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), M, N, K, code,
+                    out.data_ptr(), _stream_handle(stream))
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_gemv")
+    return out
+
+
+def moe_route_workspace(T, E):
+    """A workspace for moe_route on T tokens and E experts (uint8)."""
+    import torch
+    rc, nbytes = mxfp4_moe_route_workspace(T, E)
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_moe_route_workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def moe_route(x, router, top_k, renormalize=True, ids=None, weights=None, workspace=None,
+              stream=None):
+    """The router of a mixture-of-experts layer. x: bfloat16 [T, H] (rows
+    contiguous), router: bfloat16 [E, H].
+
+    Returns (ids int32 [T, top_k], weights float32 [T, top_k]): the experts
+    with the largest logits x @ router^T, largest first (of equal ones the
+    lowest index first), and their softmax weights, divided by their sum
+    when `renormalize` is true.
+    """
+    import torch
+    T, H, ldx, dev = _rows(x, "x")
+    if router.dim() != 2:
+        raise ValueError("router must be 2-D [E, H]")
+    E = router.shape[0]
+    _check_on(router, "router", torch.bfloat16, (E, H), dev)
+    top_k = int(top_k)
+    rc, nbytes = mxfp4_moe_route_workspace(T, E)
+    if rc != 0 or top_k < 1:
+        raise Mxfp4Error(rc or -1, "mxfp4_moe_route")
+    if ids is None:
+        ids = _new((T, top_k), torch.int32, x.device, stream)
+    else:
+        _check_on(ids, "ids", torch.int32, (T, top_k), dev)
+    if weights is None:
+        weights = _new((T, top_k), torch.float32, x.device, stream)
+    else:
+        _check_on(weights, "weights", torch.float32, (T, top_k), dev)
+    ws = _scratch(nbytes, workspace, x.device, stream)
+    rc = mxfp4_moe_route(x.data_ptr(), ldx, router.data_ptr(), T, H, E, top_k,
+                         1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
+                         ws.data_ptr(), _stream_handle(stream))
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_moe_route")
+    return ids, weights
+
+
+def moe_workspace(T, I, top_k):
+    """A workspace for moe on T tokens, top_k experts each, of width I (uint8)."""
+    import torch
+    rc, nbytes = mxfp4_moe_workspace(T, I, top_k)
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_moe_workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def moe(x, ids, weights, w13_codes, w13_scales, w2_codes, w2_scales, out_dtype=None, out=None,
+        workspace=None, stream=None):
+    """The experts of a mixture-of-experts layer for T routed tokens:
+    y[t] = sum_j weights[t, j] * W2_e (silu(Wg_e x[t]) * (Wu_e x[t])), with
+    e = ids[t, j]; ids outside 0 .. E - 1 add nothing.
+
+    x: bfloat16 [T, H] (rows contiguous); ids int32 and weights float32
+    [T, top_k]; per expert the stacked [W_gate; W_up] in MXFP4, w13_codes
+    [E, 2I, H/2], w13_scales [E, 2I, H/32], and w2_codes [E, H, I/2],
+    w2_scales [E, H, I/32] (quantize of the weights as [E * rows, K]).
+    out_dtype: torch.bfloat16 (default) or torch.float32.
+    """
+    import torch
+    T, H, ldx, dev = _rows(x, "x")
+    if ids.dim() != 2 or w13_codes.dim() != 3 or w2_codes.dim() != 3:
+        raise ValueError("ids must be 2-D [T, top_k] and the expert weights 3-D")
+    top_k = ids.shape[1]
+    E, I = w13_codes.shape[0], w2_codes.shape[2] * 2
+    _check_on(ids, "ids", torch.int32, (T, top_k), dev)
+    _check_on(weights, "weights", torch.float32, (T, top_k), dev)
+    _check_on(w13_codes, "w13_codes", torch.uint8, (E, 2 * I, H // 2), dev)
+    _check_on(w13_scales, "w13_scales", torch.uint8, (E, 2 * I, H // 32), dev)
+    _check_on(w2_codes, "w2_codes", torch.uint8, (E, H, I // 2), dev)
+    _check_on(w2_scales, "w2_scales", torch.uint8, (E, H, I // 32), dev)
+    out_dtype, code = _out_code(out_dtype, out)
+    if out is None:
+        out = _new((T, H), out_dtype, x.device, stream)
+    else:
+        _check_on(out, "out", out_dtype, (T, H), dev)
+    rc, nbytes = mxfp4_moe_workspace(T, I, top_k)
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_moe")
+    ws = _scratch(nbytes, workspace, x.device, stream)
+    rc = mxfp4_moe(x.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), w13_codes.data_ptr(),
+                   w13_scales.data_ptr(), w2_codes.data_ptr(), w2_scales.data_ptr(), T, H, I, E,
+                   top_k, code, out.data_ptr(), ws.data_ptr(), _stream_handle(stream))
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_moe")
     return out

@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxfp4.so")
 SOURCES = ["api.hip", "quantize.hip", "quantize_sr.hip", "quantize2d.hip", "gemm.hip",
-           "gemm_skinny.hip", "shuffle.hip"]
+           "gemm_skinny.hip", "shuffle.hip", "api_fewtoken.hip", "gemv.hip", "moe_route.hip",
+           "moe.hip"]
 ARCH = "gfx950"
 
 

@@ -47,6 +47,7 @@ from .frag import (  # noqa: F401
     to_frag,
     from_frag,
 )
+from . import fewtoken  # noqa: F401
 from .compare import (  # noqa: F401
     FP32_REL_TOL,
     fp32_rel_tol,

@@ -1,14 +1,10 @@
-// Shared by the few-token kernels (gemv.hip, moe.hip): the product of 16
-// MXFP4 weight rows with up to 16 BF16 activation rows on
-// v_mfma_f32_16x16x32_bf16, and the launchers that api_fewtoken.hip calls.
+// Shared by the few-token kernels (gemv.hip, moe.hip): products of MXFP4
+// weight rows with a few activation rows, and the launchers that
+// api_fewtoken.hip calls.
 //
-// Operands. The weight rows are the MFMA's first operand and the activation
-// rows ("tokens") its second: lane l holds 8 consecutive k of weight row
-// l % 16 and of token l % 16, both for the K group l / 16, and accumulator
-// register v of lane l is output (row 4 (l / 16) + v, token l % 16). The
-// sum over k does not care which k the four groups stand for, so group g
-// takes whole 32-element blocks: one 16-byte load is the codes of one block
-// of the lane's row, and its 8-element quarters feed four MFMAs.
+// One activation row: 64 lanes stream whole lines of a weight row and
+// multiply their blocks on the VALU. Several: few_stream, on
+// v_mfma_f32_16x16x32_bf16.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,8 +17,11 @@ namespace mxfp4 {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
-constexpr int kFewTile = 16;        // weight rows and tokens of one MFMA
-constexpr int kFewChunkBlocks = 8;  // 32-element blocks a wave takes per step (256 k)
+constexpr int kFewTile = 16;  // weight rows and activation rows of one MFMA
+
+__device__ __forceinline__ float scale_of_byte(uint32_t byte) {
+  return __uint_as_float(byte << 23);
+}
 
 // Eight E2M1 codes (element 2i in bits 3:0 of byte i) times 2^(byte - 127),
 // in BF16, exact; scale carries the UE8M0 byte in its float exponent field.
@@ -34,55 +33,259 @@ __device__ __forceinline__ bf16x8_t decode8(uint32_t w, float scale) {
   return (bf16x8_t){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ float scale_of_byte(uint32_t byte) {
-  return __uint_as_float(byte << 23);
+// Orders the LDS accesses of one wave's lanes among each other.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
-// Adds the product over the K chunks c0, c0 + cs, ... of KB blocks to acc
-// for kRT row tiles that share the token rows. codes[i], scales[i]: the
-// lane's row of tile i; x: the lane's token row; g: the lane's K group.
-template <int kRT>
-__device__ __forceinline__ void few_mac(const uint8_t* const (&codes)[kRT],
-                                        const uint8_t* const (&scales)[kRT], const uint8_t* x,
-                                        int KB, int c0, int cs, int g, v4f_t (&acc)[kRT]) {
-  const int chunks = (KB + kFewChunkBlocks - 1) / kFewChunkBlocks;
-  for (int c = c0; c < chunks; c += cs) {
+// ------------------------------------------------------ one activation row
+// Lane sums of four rows -> the row r's total in lanes 16 r .. 16 r + 15.
+__device__ __forceinline__ float sum_four_rows(const float (&v)[4]) {
+  const auto merge32 = [](float a, float b) {  // low half: a's, high half: b's
+    const auto s =
+        __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  };
+  const float a = merge32(v[0], v[2]), b = merge32(v[1], v[3]);
+  const auto s =
+      __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  float sum = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  const auto rotated = [](float f, auto ctrl) {  // within 16 lanes
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(f), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  sum += rotated(sum, std::integral_constant<int, 0x128>{});
+  sum += rotated(sum, std::integral_constant<int, 0x124>{});
+  sum += rotated(sum, std::integral_constant<int, 0x122>{});
+  sum += rotated(sum, std::integral_constant<int, 0x121>{});
+  return sum;
+}
+
+// acc + the product of a block's 32 codes with 32 BF16 activations.
+__device__ __forceinline__ float dot_block(u32x4_t w, float scale, const u32x4_t (&x)[4],
+                                           float acc) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      // Blocks past the row are read as block KB - 1 and count as zeros on
-      // both sides.
-      const int b = c * kFewChunkBlocks + 2 * g + j;
-      const bool in = b < KB;
-      const int bb = in ? b : KB - 1;
-      u32x4_t w[kRT], xv[4];
-      float s[kRT];
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t ww = w[q], x0 = x[q][0], x1 = x[q][1], x2 = x[q][2], x3 = x[q][3];
+    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww, scale, 0),
+                                          as_bf16x2(x0), acc, false);
+    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww, scale, 1),
+                                          as_bf16x2(x1), acc, false);
+    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww, scale, 2),
+                                          as_bf16x2(x2), acc, false);
+    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww, scale, 3),
+                                          as_bf16x2(x3), acc, false);
+  }
+  return acc;
+}
+
+// --------------------------------------------------- several activation rows
+// Work of a wave: units of 256 k (8 blocks) of T tiles of 16 weight rows and
+// of up to 16 activation columns. Everything is fetched as whole lines (8
+// weight rows x 128 B an instruction, X's activations alike), one unit ahead
+// of its use, parked in the wave's own LDS and read back as the MFMA's
+// fragments: lane l has row l % 16's dword l / 16 of a block (8 codes) and
+// the same 8 k of activation column l % 16, so accumulator register v of
+// lane l is output (weight row 4 (l / 16) + v, column l % 16).
+// Loading fragments straight from the rows touches 16 to 32 lines an
+// instruction: 8 x 4096 x 14336 12.0 us against 8.6 us, 16 x 28672 x 4096
+// 20 us against 16.5-17.1 us. Two, three or four units ahead measured no
+// faster at any shape, and slower where the registers cost waves.
+constexpr int kUnitBlocks = 8;
+constexpr int kXStride = 256 + 16;  // LDS row strides: padded, so that the
+constexpr int kWStride = 128 + 16;  // fragment reads meet no bank conflicts
+
+// Activations for few_stream: 4 XL BF16 rows, one a column. Lane l loads rows
+// 4 i + l / 16, 16 bytes each.
+template <int XL>
+struct BfRows {
+  static constexpr int kColumns = 4 * XL;
+  struct Half {
+    u32x4_t r[XL];
+  };
+  const uint8_t* p[XL];  // the lane's rows, plus its place in a block (l % 4) * 16
+
+  // Half h (128 k) of unit u; blocks past the row are read as its last.
+  __device__ __forceinline__ void load(Half& a, int u, int h, int KB) const {
+    const int b = min(u * kUnitBlocks + h * 4 + (int)((threadIdx.x & 15) >> 2), KB - 1);
 #pragma unroll
-      for (int i = 0; i < kRT; ++i) {
-        w[i] = *reinterpret_cast<const u32x4_t*>(codes[i] + (int64_t)bb * 16);
-        s[i] = scale_of_byte(scales[i][bb]);
-      }
+    for (int i = 0; i < XL; ++i)
+      a.r[i] = *reinterpret_cast<const u32x4_t*>(p[i] + (int64_t)b * 64);
+  }
+  // Zeros in place of the blocks from nb of the unit.
+  __device__ __forceinline__ void cut(Half& a, int h, int nb) const {
+    if (h * 4 + (int)((threadIdx.x & 15) >> 2) >= nb) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        xv[q] = *reinterpret_cast<const u32x4_t*>(x + (int64_t)bb * 64 + 16 * q);
-      if (!in) {
+      for (int i = 0; i < XL; ++i) a.r[i] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+  }
+  __device__ __forceinline__ void park(const Half& a, uint8_t* lds) const {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-          w[i] = u32x4_t{0u, 0u, 0u, 0u};
-          s[i] = 1.0f;
+    for (int i = 0; i < XL; ++i)
+      *reinterpret_cast<u32x4_t*>(lds + (4 * i + (lane >> 4)) * kXStride + (lane & 15) * 16) =
+          a.r[i];
+  }
+};
+
+// Activations for few_stream: kRows (even) FP32 rows, each as the sum of
+// kPieces BF16 values in columns piece * kRows + row. Every rounding leaves a
+// rest that FP32 holds exactly, at most 2^-9 of the value, so two pieces give
+// 16 bits of significand and three all 24 (values below 2^-100 fewer). Lane l
+// loads rows 2 i + l / 32, 4 values each.
+template <int kRows, int kPieces>
+struct F32Rows {
+  static constexpr int kColumns = kRows * kPieces;
+  struct Half {
+    v4f_t r[kRows / 2];
+  };
+  const float* p[kRows / 2];  // the lane's rows, plus its place in a block (l % 8) * 4
+
+  __device__ __forceinline__ void load(Half& a, int u, int h, int KB) const {
+    const int b = min(u * kUnitBlocks + h * 4 + (int)((threadIdx.x & 31) >> 3), KB - 1);
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i)
+      a.r[i] = *reinterpret_cast<const v4f_t*>(p[i] + (int64_t)b * 32);
+  }
+  __device__ __forceinline__ void cut(Half& a, int h, int nb) const {
+    if (h * 4 + (int)((threadIdx.x & 31) >> 3) >= nb) {
+#pragma unroll
+      for (int i = 0; i < kRows / 2; ++i) a.r[i] = v4f_t{};
+    }
+  }
+  __device__ __forceinline__ void park(const Half& a, uint8_t* lds) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) {
+      float v[4] = {a.r[i][0], a.r[i][1], a.r[i][2], a.r[i][3]};
+#pragma unroll
+      for (int piece = 0; piece < kPieces; ++piece) {
+        const uint32_t w0 = pack_bf16x2(v[0], v[1]), w1 = pack_bf16x2(v[2], v[3]);
+        *reinterpret_cast<uint2*>(lds + (piece * kRows + 2 * i + (lane >> 5)) * kXStride +
+                                  (lane & 31) * 8) = make_uint2(w0, w1);
+        if (piece + 1 < kPieces) {
+          // No rest where the piece is no finite number: inf - inf is NaN.
+          const uint32_t bits[4] = {w0 << 16, w0 & 0xFFFF0000u, w1 << 16, w1 & 0xFFFF0000u};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = (bits[j] & 0x7F800000u) == 0x7F800000u ? 0.0f : v[j] - __uint_as_float(bits[j]);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) xv[q] = u32x4_t{0u, 0u, 0u, 0u};
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bf16x8_t xb = __builtin_bit_cast(bf16x8_t, xv[q]);
-#pragma unroll
-        for (int i = 0; i < kRT; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(w[i][q], s[i]), xb, acc[i], 0,
-                                                           0, 0);
       }
     }
   }
+};
+
+template <int T, class X>
+constexpr int few_lds_bytes() {  // per wave
+  return X::kColumns * kXStride + T * kFewTile * kWStride;
+}
+
+// Adds to acc the products over the units first, first + stride, ... of rows
+// row(t, 0 .. 15), counted from codes[t] and scales[t] (KB blocks a row; both
+// pointers the same in every lane, the rows' bytes within 2^32 of them).
+template <int T, class X, class Row>
+__device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
+                                           const uint8_t* const (&scales)[T], const Row& row,
+                                           const X& x, int KB, int first, int stride, uint8_t* lds,
+                                           v4f_t (&acc)[T]) {
+  const int lane = threadIdx.x & 63;
+  const int a = lane & 15, g = lane >> 4, blk = lane & 7;
+  const int column = min(a, X::kColumns - 1);
+  uint8_t* xl = lds;
+  uint8_t* wl = lds + X::kColumns * kXStride;
+  uint32_t cp[T][2], sp[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) cp[t][d] = (uint32_t)row(t, 8 * d + (lane >> 3)) * KB * 16;
+    sp[t] = (uint32_t)row(t, a) * KB;
+  }
+  const int units = (KB + kUnitBlocks - 1) / kUnitBlocks;
+  if (first >= units) return;
+  u32x4_t w[T][2];
+  uint64_t sc[T];
+  typename X::Half xr[2];
+
+  // Blocks past the row are read as its last and taken as zeros when used.
+  // The eight scale bytes are those that end with the row's last.
+  const auto load = [&](int u) {
+    const uint32_t at = (uint32_t)min(u * kUnitBlocks + blk, KB - 1) * 16;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        w[t][d] = *reinterpret_cast<const u32x4_t*>(codes[t] + (cp[t][d] + at));
+    if (KB >= kUnitBlocks) {
+      const uint32_t from = (uint32_t)min(u * kUnitBlocks, KB - kUnitBlocks);
+#pragma unroll
+      for (int t = 0; t < T; ++t) __builtin_memcpy(&sc[t], scales[t] + (sp[t] + from), 8);
+    } else {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        sc[t] = 0;
+        for (int i = 0; i < KB; ++i)
+          sc[t] |= (uint64_t)scales[t][sp[t] + i] << (8 * (kUnitBlocks - KB + i));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x.load(xr[h], u, h, KB);
+  };
+
+  load(first);
+  for (int u = first; u < units; u += stride) {
+    const int nb = KB - u * kUnitBlocks;
+    uint64_t cs[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        *reinterpret_cast<u32x4_t*>(wl + (t * kFewTile + 8 * d + (lane >> 3)) * kWStride +
+                                    blk * 16) = w[t][d];
+      cs[t] = sc[t];
+    }
+    if (nb < kUnitBlocks) {
+      // Scale 1 and activations of zero for what is past the row.
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        cs[t] = (cs[t] >> (8 * (kUnitBlocks - nb))) | (0x7F7F7F7F7F7F7F7Full << (8 * nb));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x.cut(xr[h], h, nb);
+    }
+    x.park(xr[0], xl);
+    const typename X::Half x1 = xr[1];
+    if (u + stride < units) load(u + stride);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1) {
+        wave_sync();
+        x.park(x1, xl);
+      }
+      wave_sync();
+      bf16x8_t xf[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        xf[b] = *reinterpret_cast<const bf16x8_t*>(xl + column * kXStride + b * 64 + g * 16);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const uint32_t c4 = (uint32_t)(cs[t] >> (32 * h));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t ww = *reinterpret_cast<const uint32_t*>(
+              wl + (t * kFewTile + a) * kWStride + (4 * h + b) * 16 + 4 * g);
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              decode8(ww, scale_of_byte((c4 >> (8 * b)) & 0xFF)), xf[b], acc[t], 0, 0, 0);
+        }
+      }
+    }
+    wave_sync();
+  }
+}
+
+// Waves that share `items` evenly, of at most `most`.
+inline int even_waves(int items, int most) {
+  const int rounds = (items + most - 1) / most;
+  return (items + rounds - 1) / rounds;
 }
 
 // Launchers: arguments are validated by the caller.

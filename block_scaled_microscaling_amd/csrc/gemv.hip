@@ -6,10 +6,6 @@
 //
 // What bounds it: the weight's 17/32 byte per element is read once, for 2 M
 // flop per element: HBM for every M here.
-//
-// Work split: a workgroup of 8 waves owns 16 weight rows and 16 tokens; the
-// K chunks go round the waves and the 8 partial tiles are summed in LDS in
-// wave order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,62 +14,160 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kMaxWaves = 8;
 
 template <bool kOutFp32>
-__global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restrict__ x, int64_t ldx,
-                                                        const uint8_t* __restrict__ codes,
-                                                        const uint8_t* __restrict__ scales, int M,
-                                                        int N, int KB, void* __restrict__ y) {
-  __shared__ __align__(16) float red[kWaves * 256];
+__device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
+  if constexpr (kOutFp32)
+    static_cast<float*>(y)[at] = v;
+  else
+    static_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16x2(v, v);
+}
+
+// One row of x. A wave takes 64 blocks (2048 k) of four weight rows, a block
+// a lane: each load is 1 KiB of one row, all of them are issued at once, and
+// the waves of a workgroup are the segments of K. Four rows rather than 8 or
+// 16: 8192 x 8192 7.4 us against 7.7 and 8.4; the MFMA kernel below 9.4.
+constexpr int kOneRows = 4;
+
+template <bool kOutFp32>
+__global__ __launch_bounds__(64 * kMaxWaves) void gemv_one_kernel(
+    const uint8_t* __restrict__ x, const uint8_t* __restrict__ codes,
+    const uint8_t* __restrict__ scales, int N, int KB, void* __restrict__ y) {
+  __shared__ float red[kMaxWaves * kOneRows];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int n0 = blockIdx.x * kFewTile;
-  const int m0 = blockIdx.y * kFewTile;
-  // Rows and tokens past the end re-read the last one; they are not stored.
-  const int n = min(n0 + (lane & 15), N - 1);
-  const int m = min(m0 + (lane & 15), M - 1);
-  const uint8_t* wc[1] = {codes + (int64_t)n * KB * 16};
-  const uint8_t* ws[1] = {scales + (int64_t)n * KB};
-  v4f_t acc[1] = {v4f_t{}};
-  few_mac<1>(wc, ws, x + (int64_t)m * ldx * 2, KB, wave, kWaves, lane >> 4, acc);
-  // Output (row 4 g + v, token t) at 64 v + 16 g + t of the wave's part.
+  const int waves = blockDim.x >> 6;
+  const int64_t n0 = (int64_t)blockIdx.x * kOneRows;
+  float acc[kOneRows] = {};
+  for (int s = wave; s * 64 < KB; s += waves) {
+    const bool in = s * 64 + lane < KB;
+    const int b = in ? s * 64 + lane : KB - 1;
+    u32x4_t w[kOneRows], xv[4];
+    uint32_t byte[kOneRows];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) red[wave * 256 + v * 64 + lane] = acc[0][v];
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    // Thread i: row i % 16 of token i / 16, so a token's rows store together.
-    const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-    const int at = (r & 3) * 64 + (r >> 2) * 16 + t;
-    float sum = red[at];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += red[w * 256 + at];
-    if (n0 + r < N && m0 + t < M) {
-      const int64_t o = (int64_t)(m0 + t) * N + n0 + r;
-      if constexpr (kOutFp32)
-        static_cast<float*>(y)[o] = sum;
-      else
-        static_cast<uint16_t*>(y)[o] = (uint16_t)pack_bf16x2(sum, sum);
+    for (int r = 0; r < kOneRows; ++r) {
+      const int64_t n = min(n0 + r, (int64_t)N - 1);  // rows past the end are not stored
+      w[r] = *reinterpret_cast<const u32x4_t*>(codes + n * KB * 16 + (int64_t)b * 16);
+      byte[r] = scales[n * KB + b];
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      xv[q] = *reinterpret_cast<const u32x4_t*>(x + (int64_t)b * 64 + 16 * q);
+    if (!in) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) xv[q] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int r = 0; r < kOneRows; ++r)
+      acc[r] = dot_block(w[r], scale_of_byte(in ? byte[r] : 127u), xv, acc[r]);
   }
+  const float sum = sum_four_rows(acc);
+  if ((lane & 15) == 0) red[wave * kOneRows + (lane >> 4)] = sum;
+  __syncthreads();
+  if (threadIdx.x < kOneRows && n0 + threadIdx.x < N) {
+    float v = red[threadIdx.x];
+    for (int w = 1; w < waves; ++w) v += red[w * kOneRows + threadIdx.x];
+    store_y<kOutFp32>(y, n0 + threadIdx.x, v);
+  }
+}
+
+// Several rows of x: a workgroup owns T tiles of 16 weight rows and up to 16
+// rows of x, its waves take the units of 256 k in turn, and the partial tiles
+// are summed in LDS in wave order.
+template <int T, int XL, bool kOutFp32>
+__global__ __launch_bounds__(64 * kMaxWaves) void gemv_few_kernel(
+    const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ codes,
+    const uint8_t* __restrict__ scales, int M, int N, int KB, void* __restrict__ y) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int64_t n0 = (int64_t)blockIdx.x * (T * kFewTile);
+  const int m0 = blockIdx.y * kFewTile;
+  const int last = (int)min((int64_t)N - 1 - n0, (int64_t)(T * kFewTile - 1));
+  const uint8_t* wc[T];
+  const uint8_t* ws[T];
+  v4f_t acc[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    wc[t] = codes + n0 * KB * 16;
+    ws[t] = scales + n0 * KB;
+    acc[t] = v4f_t{};
+  }
+  BfRows<XL> rows;
+#pragma unroll
+  for (int i = 0; i < XL; ++i)
+    rows.p[i] = x + (int64_t)min(m0 + 4 * i + (lane >> 4), M - 1) * ldx * 2 + (lane & 3) * 16;
+  // Rows past the end re-read the last one; they are not stored.
+  few_stream<T>(wc, ws, [&](int t, int r) { return min(kFewTile * t + r, last); }, rows, KB, wave,
+                waves, lds + wave * few_lds_bytes<T, BfRows<XL>>(), acc);
+  __syncthreads();
+  auto* red = reinterpret_cast<float*>(lds);
+  // Output (row 4 g + v, column c) at 64 v + 16 g + c of the wave's part.
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[(t * waves + wave) * 256 + v * 64 + lane] = acc[t][v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < T * 256; i += blockDim.x) {
+    // Row i % 16 of column i / 16 % 16, so a token's rows store together.
+    const int t = i >> 8, r = i & 15, c = (i >> 4) & 15;
+    const float* part = red + t * waves * 256 + (r & 3) * 64 + (r >> 2) * 16 + c;
+    float v = part[0];
+    for (int w = 1; w < waves; ++w) v += part[w * 256];
+    if (kFewTile * t + r <= last && c < 4 * XL && m0 + c < M)
+      store_y<kOutFp32>(y, (int64_t)(m0 + c) * N + n0 + kFewTile * t + r, v);
+  }
+}
+
+template <int T, int XL>
+hipError_t launch_few(const uint8_t* x, int64_t ldx, const uint8_t* codes, const uint8_t* scales,
+                      int M, int N, int KB, int most, bool out_fp32, void* y,
+                      hipStream_t stream) {
+  const int waves = even_waves((KB + kUnitBlocks - 1) / kUnitBlocks, most);
+  // The partial tiles (T KiB a wave) take the place of what was streamed.
+  static_assert(few_lds_bytes<T, BfRows<XL>>() >= T * 1024, "");
+  const int lds = waves * few_lds_bytes<T, BfRows<XL>>();
+  const dim3 grid((uint32_t)(((int64_t)N + T * kFewTile - 1) / (T * kFewTile)),
+                  (M + kFewTile - 1) / kFewTile);
+  const auto kernel = out_fp32 ? gemv_few_kernel<T, XL, true> : gemv_few_kernel<T, XL, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds, stream, x, ldx, codes, scales, M, N, KB,
+                     y);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gemv(const void* x, int64_t ldx, const void* codes, const void* scales, int M,
                        int N, int K, bool out_fp32, void* y, hipStream_t stream) {
-  const dim3 grid((uint32_t)(((int64_t)N + kFewTile - 1) / kFewTile), (M + kFewTile - 1) / kFewTile);
   const auto* xb = static_cast<const uint8_t*>(x);
   const auto* wc = static_cast<const uint8_t*>(codes);
   const auto* ws = static_cast<const uint8_t*>(scales);
-  if (out_fp32)
-    hipLaunchKernelGGL((gemv_kernel<true>), grid, dim3(kThreads), 0, stream, xb, ldx, wc, ws, M, N,
-                       K / 32, y);
-  else
-    hipLaunchKernelGGL((gemv_kernel<false>), grid, dim3(kThreads), 0, stream, xb, ldx, wc, ws, M,
-                       N, K / 32, y);
-  return hipGetLastError();
+  const int KB = K / 32;
+  if (M == 1) {
+    const dim3 grid((uint32_t)(((int64_t)N + kOneRows - 1) / kOneRows));
+    const dim3 threads(64 * even_waves((KB + 63) / 64, kMaxWaves));
+    if (out_fp32)
+      hipLaunchKernelGGL((gemv_one_kernel<true>), grid, threads, 0, stream, xb, wc, ws, N, KB, y);
+    else
+      hipLaunchKernelGGL((gemv_one_kernel<false>), grid, threads, 0, stream, xb, wc, ws, N, KB, y);
+    return hipGetLastError();
+  }
+  // Two tiles a workgroup halve the reads of x from L2 but also the
+  // workgroups: from 384 tiles on (1.5 a CU) they pay (5 rows x 6177 x 7968
+  // 9.0 against 9.8 us, 16 x 8192 x 8192 11.3 against 12.6), below not (8 x
+  // 4096 x 14336 10.8 against 8.6, 16 x 2048 x 2048 4.1 against 3.4). With 16
+  // rows of x and two tiles, four waves leave room for a second workgroup's
+  // LDS and registers (16 x 28672 x 4096: 17.1 against 22.1 us). Up to four
+  // rows x is small and one tile is never slower by more than 1%.
+  const int64_t tiles = (((int64_t)N + kFewTile - 1) / kFewTile) * ((M + kFewTile - 1) / kFewTile);
+  if (M <= 4) return launch_few<1, 1>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream);
+  if (tiles < 384)
+    return M <= 8 ? launch_few<1, 2>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream)
+                  : launch_few<1, 4>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream);
+  return M <= 8 ? launch_few<2, 2>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream)
+                : launch_few<2, 4>(xb, ldx, wc, ws, M, N, KB, 4, out_fp32, y, stream);
 }
 
 }  // namespace mxfp4

@@ -33,6 +33,55 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMapWords = kMaxExperts / 32;
 constexpr int kLdsSlots = 1024;  // pair results held at once, 16 outputs each
 
+constexpr int kFewChunkBlocks = 8;  // 32-element blocks a wave takes per step (256 k)
+
+// Adds the product over the K chunks c0, c0 + cs, ... of KB blocks to acc
+// for kRT row tiles that share the token rows. codes[i], scales[i]: the
+// lane's row of tile i; x: the lane's token row; g: the lane's K group.
+template <int kRT>
+__device__ __forceinline__ void few_mac(const uint8_t* const (&codes)[kRT],
+                                        const uint8_t* const (&scales)[kRT], const uint8_t* x,
+                                        int KB, int c0, int cs, int g, v4f_t (&acc)[kRT]) {
+  const int chunks = (KB + kFewChunkBlocks - 1) / kFewChunkBlocks;
+  for (int c = c0; c < chunks; c += cs) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      // Blocks past the row are read as block KB - 1 and count as zeros on
+      // both sides.
+      const int b = c * kFewChunkBlocks + 2 * g + j;
+      const bool in = b < KB;
+      const int bb = in ? b : KB - 1;
+      u32x4_t w[kRT], xv[4];
+      float s[kRT];
+#pragma unroll
+      for (int i = 0; i < kRT; ++i) {
+        w[i] = *reinterpret_cast<const u32x4_t*>(codes[i] + (int64_t)bb * 16);
+        s[i] = scale_of_byte(scales[i][bb]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        xv[q] = *reinterpret_cast<const u32x4_t*>(x + (int64_t)bb * 64 + 16 * q);
+      if (!in) {
+#pragma unroll
+        for (int i = 0; i < kRT; ++i) {
+          w[i] = u32x4_t{0u, 0u, 0u, 0u};
+          s[i] = 1.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) xv[q] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bf16x8_t xb = __builtin_bit_cast(bf16x8_t, xv[q]);
+#pragma unroll
+        for (int i = 0; i < kRT; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(w[i][q], s[i]), xb, acc[i], 0,
+                                                           0, 0);
+      }
+    }
+  }
+}
+
 // The pairs and which experts they chose, in LDS.
 struct Chosen {
   int32_t ids[kMaxPairs];
@@ -71,12 +120,6 @@ __device__ __forceinline__ int count_chosen(const Chosen& c, int E) {
   int n = 0;
   for (int w = 0; w < (E + 31) / 32; ++w) n += __popc(c.map[w]);
   return n;
-}
-
-// Orders the LDS accesses of one wave's lanes among each other.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // One wave writes the pairs of expert e in ascending order; returns how many.

@@ -108,7 +108,7 @@ def load_library():
         lib.mxfp4_moe_route_workspace.restype = i32
         lib.mxfp4_moe_route.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp]
         lib.mxfp4_moe_route.restype = i32
-        lib.mxfp4_moe_workspace.argtypes = [i64, i64, i64, pi64]
+        lib.mxfp4_moe_workspace.argtypes = [i64, i64, i64, i64, pi64]
         lib.mxfp4_moe_workspace.restype = i32
         lib.mxfp4_moe.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32,
                                   vp, vp, vp]
@@ -225,10 +225,10 @@ def mxfp4_moe_route(x_bf16, ldx, router_bf16, T, H, E, top_k, renormalize, ids, 
                                               renormalize, ids, weights, workspace, stream))
 
 
-def mxfp4_moe_workspace(T, I, top_k):
+def mxfp4_moe_workspace(T, H, I, top_k):
     """(rc, bytes) of moe's workspace."""
     n = ctypes.c_int64(0)
-    rc = int(load_library().mxfp4_moe_workspace(T, I, top_k, ctypes.byref(n)))
+    rc = int(load_library().mxfp4_moe_workspace(T, H, I, top_k, ctypes.byref(n)))
     return rc, n.value
 
 
@@ -684,10 +684,10 @@ def moe_route(x, router, top_k, renormalize=True, ids=None, weights=None, worksp
     return ids, weights
 
 
-def moe_workspace(T, I, top_k):
-    """A workspace for moe on T tokens, top_k experts each, of width I (uint8)."""
+def moe_workspace(T, H, I, top_k):
+    """A workspace for moe on T tokens of H, top_k experts each, of width I (uint8)."""
     import torch
-    rc, nbytes = mxfp4_moe_workspace(T, I, top_k)
+    rc, nbytes = mxfp4_moe_workspace(T, H, I, top_k)
     if rc != 0:
         raise Mxfp4Error(rc, "mxfp4_moe_workspace")
     return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
@@ -722,7 +722,7 @@ def moe(x, ids, weights, w13_codes, w13_scales, w2_codes, w2_scales, out_dtype=N
         out = _new((T, H), out_dtype, x.device, stream)
     else:
         _check_on(out, "out", out_dtype, (T, H), dev)
-    rc, nbytes = mxfp4_moe_workspace(T, I, top_k)
+    rc, nbytes = mxfp4_moe_workspace(T, H, I, top_k)
     if rc != 0:
         raise Mxfp4Error(rc, "mxfp4_moe")
     ws = _scratch(nbytes, workspace, x.device, stream)

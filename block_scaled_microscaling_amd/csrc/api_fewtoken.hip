@@ -89,11 +89,15 @@ int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, in
       static_cast<hipStream_t>(stream)));
 }
 
-int mxfp4_moe_workspace(int64_t T, int64_t I, int64_t top_k, int64_t* bytes) {
+int mxfp4_moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top_k, int64_t* bytes) {
   if (!bytes || T < 1 || top_k < 1 || top_k > kMaxTopK || T > kMaxPairs || T * top_k > kMaxPairs)
     return MXFP4_EINVAL;
-  if (I < 32 || I % 32 != 0 || I > kMaxMoeDim) return MXFP4_EINVAL;
-  *bytes = T * top_k * 2 * I * (int64_t)sizeof(uint16_t);
+  if (H < 32 || H % 32 != 0 || H > kMaxMoeDim || I < 32 || I % 32 != 0 || I > kMaxMoeDim)
+    return MXFP4_EINVAL;
+  // The activations; with several tokens, partial sums of y and a counter per
+  // 16 of its columns.
+  *bytes = T * top_k * I * (int64_t)sizeof(float);
+  if (T > 1) *bytes += mxfp4::kMoeMaxParts * T * H * (int64_t)sizeof(float) + H / 16 * 4;
   return MXFP4_OK;
 }
 
@@ -105,8 +109,8 @@ int mxfp4_moe(const void* x_bf16, int64_t ldx, const void* ids, const void* weig
       !workspace)
     return MXFP4_EINVAL;
   int64_t bytes = 0;
-  if (mxfp4_moe_workspace(T, I, top_k, &bytes) != MXFP4_OK) return MXFP4_EINVAL;
-  if (H < 32 || H % 32 != 0 || H > kMaxMoeDim || E < 1 || E > kMaxExperts) return MXFP4_EINVAL;
+  if (mxfp4_moe_workspace(T, H, I, top_k, &bytes) != MXFP4_OK) return MXFP4_EINVAL;
+  if (E < 1 || E > kMaxExperts) return MXFP4_EINVAL;
   if (!valid_out(out_dtype) || !valid_rows(T, H, ldx)) return MXFP4_EINVAL;
   if (!below_max_bytes(E, I, H)) return MXFP4_EINVAL;
   if (!aligned(x_bf16, 16) || !aligned(ids, 4) || !aligned(weights, 4) ||
@@ -117,8 +121,7 @@ int mxfp4_moe(const void* x_bf16, int64_t ldx, const void* ids, const void* weig
   return launch_status(mxfp4::launch_moe(
       x_bf16, ldx, static_cast<const int32_t*>(ids), static_cast<const float*>(weights),
       W13_codes, W13_scales, W2_codes, W2_scales, (int)T, (int)H, (int)I, (int)E, (int)top_k,
-      out_dtype == MXFP4_OUT_FP32, y, static_cast<uint16_t*>(workspace),
-      static_cast<hipStream_t>(stream)));
+      out_dtype == MXFP4_OUT_FP32, y, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gfx950.h"
 
 namespace mxfp4 {
@@ -288,6 +290,9 @@ inline int even_waves(int items, int most) {
   return (items + rounds - 1) / rounds;
 }
 
+// Parts into which moe's second kernel splits the experts, at most.
+constexpr int kMoeMaxParts = 8;
+
 // Launchers: arguments are validated by the caller.
 hipError_t launch_gemv(const void* x, int64_t ldx, const void* codes, const void* scales, int M,
                        int N, int K, bool out_fp32, void* y, hipStream_t stream);
@@ -296,7 +301,7 @@ hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int 
                             double* logits, hipStream_t stream);
 hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const float* weights,
                       const void* w13, const void* w13_s, const void* w2, const void* w2_s, int T,
-                      int H, int I, int E, int top_k, bool out_fp32, void* y, uint16_t* act,
+                      int H, int I, int E, int top_k, bool out_fp32, void* y, void* workspace,
                       hipStream_t stream);
 
 }  // namespace mxfp4

@@ -4,20 +4,19 @@
 // Mathematics, for pair p = t top_k + j with expert e = ids[p]:
 //   a[p, i] = silu(sum_h Wg_e[i, h] x[t, h]) * (sum_h Wu_e[i, h] x[t, h])
 //   y[t, h] = sum_j weights[t, j] sum_i W2_e[h, i] a[p, i]
-// Weights are exact in BF16 and sums are FP32. a is handed to the second
-// product as hi + lo, both BF16 (hi = a rounded, lo = a - hi rounded): 16
-// significand bits, so that y's error stays that of its FP32 sums and one
-// rounding to its type. The two halves ride in different columns of the same
-// MFMA (8 pairs a time), so lo costs no further weight reads or MFMAs.
+// Weights are exact in BF16, sums and a are FP32. The second product takes a
+// as FP32 (one token) or as the sum of BF16 pieces in columns of the same
+// MFMA: three, all of FP32's significand, for FP32 results; two, 16 bits, for
+// BF16 results, whose own rounding is 2^8 times larger.
 //
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
 // once: HBM.
 //
-// Work split. First kernel: one workgroup per 16 activation columns and
-// place in the list of chosen experts; K chunks go round its 8 waves. Second
-// kernel: one workgroup per 16 outputs h and all pairs, whose results stay
-// in LDS: its waves take the chosen experts in turn, and the sum over j runs
-// in order of j, so y is the same on every run.
+// One token: as gemv's one-row kernel. The first kernel's workgroup has two
+// gate and two up rows of a pair's expert; the second's four rows of y, over
+// the blocks of all its experts in a row, so the sum over j needs no other
+// workgroup. Several tokens: an expert's weights are read once for all its
+// pairs, by few_stream.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,110 +25,144 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kMaxWaves = 8;
 constexpr int kMaxPairs = 1024;
 constexpr int kMaxExperts = 1024;
 constexpr int kMapWords = kMaxExperts / 32;
-constexpr int kLdsSlots = 1024;  // pair results held at once, 16 outputs each
+constexpr int kMaxParts = kMoeMaxParts;
 
-constexpr int kFewChunkBlocks = 8;  // 32-element blocks a wave takes per step (256 k)
+template <bool kOutFp32>
+__device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
+  if constexpr (kOutFp32)
+    static_cast<float*>(y)[at] = v;
+  else
+    static_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16x2(v, v);
+}
 
-// Adds the product over the K chunks c0, c0 + cs, ... of KB blocks to acc
-// for kRT row tiles that share the token rows. codes[i], scales[i]: the
-// lane's row of tile i; x: the lane's token row; g: the lane's K group.
-template <int kRT>
-__device__ __forceinline__ void few_mac(const uint8_t* const (&codes)[kRT],
-                                        const uint8_t* const (&scales)[kRT], const uint8_t* x,
-                                        int KB, int c0, int cs, int g, v4f_t (&acc)[kRT]) {
-  const int chunks = (KB + kFewChunkBlocks - 1) / kFewChunkBlocks;
-  for (int c = c0; c < chunks; c += cs) {
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// --------------------------------------------------------------- one token
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_one_up_kernel(
+    const uint8_t* __restrict__ x, const int32_t* __restrict__ ids,
+    const uint8_t* __restrict__ w13, const uint8_t* __restrict__ w13_s, int HB, int I, int E,
+    float* __restrict__ act) {
+  __shared__ float red[kMaxWaves * 4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int e = ids[blockIdx.y];
+  if (e < 0 || e >= E) return;
+  const int64_t gate = (int64_t)e * 2 * I + 2 * blockIdx.x;
+  const int64_t row[4] = {gate, gate + 1, gate + I, gate + I + 1};
+  float acc[4] = {};
+  for (int s = wave; s * 64 < HB; s += waves) {
+    const bool in = s * 64 + lane < HB;
+    const int b = in ? s * 64 + lane : HB - 1;
+    u32x4_t w[4], xv[4];
+    uint32_t byte[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      // Blocks past the row are read as block KB - 1 and count as zeros on
-      // both sides.
-      const int b = c * kFewChunkBlocks + 2 * g + j;
-      const bool in = b < KB;
-      const int bb = in ? b : KB - 1;
-      u32x4_t w[kRT], xv[4];
-      float s[kRT];
+    for (int r = 0; r < 4; ++r) {
+      w[r] = *reinterpret_cast<const u32x4_t*>(w13 + row[r] * HB * 16 + (int64_t)b * 16);
+      byte[r] = w13_s[row[r] * HB + b];
+    }
 #pragma unroll
-      for (int i = 0; i < kRT; ++i) {
-        w[i] = *reinterpret_cast<const u32x4_t*>(codes[i] + (int64_t)bb * 16);
-        s[i] = scale_of_byte(scales[i][bb]);
+    for (int q = 0; q < 4; ++q)
+      xv[q] = *reinterpret_cast<const u32x4_t*>(x + (int64_t)b * 64 + 16 * q);
+    if (!in) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) xv[q] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[r] = dot_block(w[r], scale_of_byte(in ? byte[r] : 127u), xv, acc[r]);
+  }
+  const float sum = sum_four_rows(acc);
+  if ((lane & 15) == 0) red[wave * 4 + (lane >> 4)] = sum;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float g = red[threadIdx.x], u = red[2 + threadIdx.x];
+    for (int w = 1; w < waves; ++w) {
+      g += red[w * 4 + threadIdx.x];
+      u += red[w * 4 + 2 + threadIdx.x];
+    }
+    act[(int64_t)blockIdx.y * I + 2 * blockIdx.x + threadIdx.x] = silu_mul(g, u);
+  }
+}
+
+template <bool kOutFp32>
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_one_down_kernel(
+    const float* __restrict__ act, const int32_t* __restrict__ ids,
+    const float* __restrict__ weights, const uint8_t* __restrict__ w2,
+    const uint8_t* __restrict__ w2_s, int H, int IB, int E, int top_k, void* __restrict__ y) {
+  __shared__ float red[kMaxWaves * 4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int h0 = blockIdx.x * 4;
+  float acc[4] = {};
+  // Block b of pair j is the (j IB + b)-th; lanes without one, and those of
+  // an absent expert, load nothing.
+  for (int s = wave; s * 64 < top_k * IB; s += waves) {
+    const int j = (s * 64 + lane) / IB, b = s * 64 + lane - j * IB;
+    const int e = j < top_k ? ids[j] : -1;
+    if (e >= 0 && e < E) {
+      u32x4_t w[4];
+      uint32_t byte[4];
+      v4f_t a[8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t row = (int64_t)e * H + h0 + r;
+        w[r] = *reinterpret_cast<const u32x4_t*>(w2 + (row * IB + b) * 16);
+        byte[r] = w2_s[row * IB + b];
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        xv[q] = *reinterpret_cast<const u32x4_t*>(x + (int64_t)bb * 64 + 16 * q);
-      if (!in) {
+      for (int q = 0; q < 8; ++q)
+        a[q] = *reinterpret_cast<const v4f_t*>(act + ((int64_t)j * IB + b) * 32 + 4 * q);
+      const float weight = weights[j];
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-          w[i] = u32x4_t{0u, 0u, 0u, 0u};
-          s[i] = 1.0f;
+      for (int r = 0; r < 4; ++r) {
+        const float scale = scale_of_byte(byte[r]);
+        float dot = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t ww = w[r][q];
+          const f32x2_t d0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 0);
+          const f32x2_t d1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 1);
+          const f32x2_t d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 2);
+          const f32x2_t d3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 3);
+          dot = fmaf(d0[0], a[2 * q][0], dot);
+          dot = fmaf(d0[1], a[2 * q][1], dot);
+          dot = fmaf(d1[0], a[2 * q][2], dot);
+          dot = fmaf(d1[1], a[2 * q][3], dot);
+          dot = fmaf(d2[0], a[2 * q + 1][0], dot);
+          dot = fmaf(d2[1], a[2 * q + 1][1], dot);
+          dot = fmaf(d3[0], a[2 * q + 1][2], dot);
+          dot = fmaf(d3[1], a[2 * q + 1][3], dot);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) xv[q] = u32x4_t{0u, 0u, 0u, 0u};
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bf16x8_t xb = __builtin_bit_cast(bf16x8_t, xv[q]);
-#pragma unroll
-        for (int i = 0; i < kRT; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(w[i][q], s[i]), xb, acc[i], 0,
-                                                           0, 0);
+        acc[r] = fmaf(weight, dot, acc[r]);
       }
     }
   }
-}
-
-// The pairs and which experts they chose, in LDS.
-struct Chosen {
-  int32_t ids[kMaxPairs];
-  uint32_t map[kMapWords];  // bit e: some pair chose expert e
-};
-
-__device__ __forceinline__ void read_chosen(Chosen& c, const int32_t* __restrict__ ids, int pairs,
-                                            int E) {
-  if (threadIdx.x < kMapWords) c.map[threadIdx.x] = 0;
+  const float sum = sum_four_rows(acc);
+  if ((lane & 15) == 0) red[wave * 4 + (lane >> 4)] = sum;
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += kThreads) {
-    const int e = ids[p];
-    const bool here = e >= 0 && e < E;
-    c.ids[p] = here ? e : -1;
-    if (here) atomicOr(&c.map[e >> 5], 1u << (e & 31));
+  if (threadIdx.x < 4) {
+    float v = red[threadIdx.x];
+    for (int w = 1; w < waves; ++w) v += red[w * 4 + threadIdx.x];
+    store_y<kOutFp32>(y, h0 + threadIdx.x, v);
   }
-  __syncthreads();
 }
 
-// The n-th chosen expert (from 0) in order of its index, or -1.
-__device__ __forceinline__ int nth_chosen(const Chosen& c, int n, int E) {
-  const int words = (E + 31) / 32;
-  for (int w = 0; w < words; ++w) {
-    uint32_t m = c.map[w];
-    const int count = __popc(m);
-    if (n < count) {
-      for (int i = 0; i < n; ++i) m &= m - 1;
-      return w * 32 + __ffs(m) - 1;
-    }
-    n -= count;
-  }
-  return -1;
-}
-
-__device__ __forceinline__ int count_chosen(const Chosen& c, int E) {
-  int n = 0;
-  for (int w = 0; w < (E + 31) / 32; ++w) n += __popc(c.map[w]);
-  return n;
-}
-
-// One wave writes the pairs of expert e in ascending order; returns how many.
-__device__ __forceinline__ int list_pairs(const Chosen& c, int pairs, int e, int lane,
-                                          uint16_t* list) {
+// ------------------------------------------------------------ several tokens
+// A wave writes the pairs of expert e in ascending order; returns how many.
+__device__ __forceinline__ int list_pairs(const int32_t* ids, int pairs, int e, uint16_t* list) {
+  const int lane = threadIdx.x & 63;
   int n = 0;
   wave_sync();
+#pragma unroll 4
   for (int base = 0; base < pairs; base += 64) {
     const int p = base + lane;
-    const bool hit = p < pairs && c.ids[p] == e;
+    const bool hit = ids[min(p, pairs - 1)] == e && p < pairs;
     const uint64_t m = __ballot(hit);
     if (hit) list[n + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)p;
     n += __popcll(m);
@@ -138,145 +171,289 @@ __device__ __forceinline__ int list_pairs(const Chosen& c, int pairs, int e, int
   return n;
 }
 
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(
-    const uint8_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
-    const uint8_t* __restrict__ w13, const uint8_t* __restrict__ w13_s, int pairs, int H, int I,
-    int E, int top_k, uint16_t* __restrict__ act) {
-  __shared__ Chosen chosen;
-  __shared__ uint16_t list[kMaxPairs];
-  __shared__ int count;
-  __shared__ __align__(16) float red[2 * kWaves * 256];
+struct UpArgs {
+  const uint8_t* x;
+  int64_t ldx;
+  const uint8_t* w13;
+  const uint8_t* w13_s;
+  float* act;
+  int HB, I, top_k;
+};
+
+// 16 activation columns of pairs list[p0 .. p0 + 4 XL): the gate and the up
+// rows are the two tiles of few_stream, K goes round the waves.
+template <int XL>
+__device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
+                                        const uint16_t* list, int p0, int n, uint8_t* lds) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  read_chosen(chosen, ids, pairs, E);
-  const int e = nth_chosen(chosen, blockIdx.y, E);
-  if (e < 0) return;
-  if (wave == 0) {
-    const int n = list_pairs(chosen, pairs, e, lane, list);
-    if (lane == 0) count = n;
+  const int waves = blockDim.x >> 6;
+  BfRows<XL> rows;
+#pragma unroll
+  for (int i = 0; i < XL; ++i) {
+    const int p = list[min(p0 + 4 * i + (lane >> 4), n - 1)];
+    rows.p[i] = g.x + (int64_t)(p / g.top_k) * g.ldx * 2 + (lane & 3) * 16;
+  }
+  const uint8_t* wc[2] = {g.w13 + gate * g.HB * 16, g.w13 + (gate + g.I) * g.HB * 16};
+  const uint8_t* ws[2] = {g.w13_s + gate * g.HB, g.w13_s + (gate + g.I) * g.HB};
+  v4f_t acc[2] = {v4f_t{}, v4f_t{}};
+  few_stream<2>(wc, ws, [](int, int r) { return r; }, rows, g.HB, wave, waves,
+                lds + wave * few_lds_bytes<2, BfRows<XL>>(), acc);
+  __syncthreads();
+  auto* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[(t * waves + wave) * 256 + v * 64 + lane] = acc[t][v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * XL; i += blockDim.x) {
+    const int r = i & 15, c = i >> 4;
+    const float* part = red + (r & 3) * 64 + (r >> 2) * 16 + c;
+    float gv = part[0], uv = part[waves * 256];
+    for (int w = 1; w < waves; ++w) {
+      gv += part[w * 256];
+      uv += part[(waves + w) * 256];
+    }
+    if (p0 + c < n) g.act[(int64_t)list[p0 + c] * g.I + i0 + r] = silu_mul(gv, uv);
   }
   __syncthreads();
-  const int n_pairs = count;
+}
+
+// One workgroup per 16 activation columns and expert. With fewer pairs than
+// experts the grid counts pairs, and the first pair of an expert stands for
+// all of its pairs. Also clears what the second kernel counts with.
+template <int kMaxXL>
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_up_kernel(
+    UpArgs g, const int32_t* __restrict__ ids, int pairs, int E, int by_pair, uint32_t* counters,
+    int n_counters) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint16_t list[kMaxPairs];
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
+  const int e = by_pair ? ids[blockIdx.y] : (int)blockIdx.y;
+  if (e < 0 || e >= E) return;
+  // Every wave writes the same list.
+  const int n = list_pairs(ids, pairs, e, list);
+  if (n == 0 || (by_pair && list[0] != blockIdx.y)) return;
   const int i0 = blockIdx.x * kFewTile;
-  const int HB = H / 32;
-  const int64_t gate = (int64_t)e * 2 * I + i0 + (lane & 15);
-  const uint8_t* wc[2] = {w13 + gate * HB * 16, w13 + (gate + I) * HB * 16};
-  const uint8_t* ws[2] = {w13_s + gate * HB, w13_s + (gate + I) * HB};
-  for (int p0 = 0; p0 < n_pairs; p0 += kFewTile) {
-    const int mine = list[min(p0 + (lane & 15), n_pairs - 1)];
-    v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-    few_mac<2>(wc, ws, x + (int64_t)(mine / top_k) * ldx * 2, HB, wave, kWaves, lane >> 4, acc);
-    if (p0 > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[(i * kWaves + wave) * 256 + v * 64 + lane] = acc[i][v];
-    __syncthreads();
-    if (threadIdx.x < 256) {
-      const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-      const int at = (r & 3) * 64 + (r >> 2) * 16 + t;
-      float g = red[at], u = red[kWaves * 256 + at];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
-        g += red[w * 256 + at];
-        u += red[(kWaves + w) * 256 + at];
-      }
-      if (p0 + t < n_pairs) {
-        const float a = g / (1.0f + expf(-g)) * u;
-        const uint32_t hi = pack_bf16x2(a, a) & 0xFFFFu;
-        // lo is 0 where hi is no finite number: inf - inf would make it NaN.
-        const float rest = (hi & 0x7F80u) == 0x7F80u ? 0.0f : a - __uint_as_float(hi << 16);
-        uint16_t* o = act + (int64_t)list[p0 + t] * 2 * I + i0 + r;
-        o[0] = (uint16_t)hi;
-        o[I] = (uint16_t)pack_bf16x2(rest, rest);
-      }
-    }
+  const int64_t gate = (int64_t)e * 2 * g.I + i0;
+  for (int p0 = 0; p0 < n; p0 += 4 * kMaxXL) {
+    const int left = n - p0;
+    if (left <= 4)
+      up_tile<1>(g, gate, i0, list, p0, n, lds);
+    else if (kMaxXL == 2 || left <= 8)
+      up_tile<2>(g, gate, i0, list, p0, n, lds);
+    else
+      up_tile<kMaxXL>(g, gate, i0, list, p0, n, lds);
   }
 }
 
-template <bool kOutFp32>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(
-    const uint16_t* __restrict__ act, const int32_t* __restrict__ ids,
+// The chosen experts as a bit map, and the pairs' experts (-1: absent).
+__device__ __forceinline__ void read_chosen(const int32_t* __restrict__ ids, int pairs, int E,
+                                            int32_t* chosen, uint32_t* map) {
+  if (threadIdx.x < kMapWords) map[threadIdx.x] = 0;
+  __syncthreads();
+  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
+    const int e = ids[p];
+    const bool here = e >= 0 && e < E;
+    chosen[p] = here ? e : -1;
+    if (here) atomicOr(&map[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+}
+
+// The n-th chosen expert (from 0) in order of its index, of more than n.
+__device__ __forceinline__ int nth_chosen(const uint32_t* map, int n) {
+  int w = 0;
+  for (; n >= __popc(map[w]); ++w) n -= __popc(map[w]);
+  uint32_t m = map[w];
+  for (int i = 0; i < n; ++i) m &= m - 1;
+  return w * 32 + __ffs(m) - 1;
+}
+
+// One workgroup per 16 outputs h and part of the chosen experts (every
+// gridDim.y-th). Its waves take the experts in turn, with few experts also
+// the units of K; the pairs' results stay in LDS and are summed in order of
+// j. The last workgroup of an h to finish adds the parts, in order of part,
+// so y is the same on every run.
+template <int kRows, int kPieces, bool kOutFp32>
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_down_kernel(
+    const float* __restrict__ act, const int32_t* __restrict__ ids,
     const float* __restrict__ weights, const uint8_t* __restrict__ w2,
     const uint8_t* __restrict__ w2_s, int T, int H, int I, int E, int top_k, int max_split,
-    void* __restrict__ y) {
-  extern __shared__ __align__(16) float part[];  // [split][pair][16]
-  __shared__ Chosen chosen;
-  __shared__ uint16_t lists[kWaves][kMaxPairs];
+    float* __restrict__ partial, uint32_t* __restrict__ counters, void* __restrict__ y) {
+  using X = F32Rows<kRows, kPieces>;
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint32_t map[kMapWords];
+  __shared__ uint32_t arrived;
+  const int pairs = T * top_k;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int pairs = T * top_k;
-  read_chosen(chosen, ids, pairs, E);
-  const int experts = count_chosen(chosen, E);
-  // With fewer experts than waves the K chunks of each go round `split` waves.
-  int split = 1;
-  while (2 * split <= max_split && 2 * split * experts <= kWaves) split *= 2;
+  const int waves = blockDim.x >> 6;
+  auto* part = reinterpret_cast<float*>(lds + waves * few_lds_bytes<1, X>());  // [split][pair][16]
+  auto* chosen = reinterpret_cast<int32_t*>(part + max_split * pairs * 16);
+  auto* list = reinterpret_cast<uint16_t*>(chosen + pairs) + wave * pairs;
+  read_chosen(ids, pairs, E, chosen, map);
+  int experts = 0;
+  for (int w = 0; w < (E + 31) / 32; ++w) experts += __popc(map[w]);
+  const int parts = gridDim.y, mine = blockIdx.y;
+  const int held = (experts - mine + parts - 1) / parts;  // experts of this part
   const int h0 = blockIdx.x * kFewTile;
   const int IB = I / 32;
-  for (int item = wave; item < experts * split; item += kWaves) {
+  int split = 1;
+  while (2 * split <= max_split && 2 * split * held <= waves) split *= 2;
+  for (int item = wave; item < held * split; item += waves) {
     const int s = item % split;
-    const int e = nth_chosen(chosen, item / split, E);
-    const int n_pairs = list_pairs(chosen, pairs, e, lane, lists[wave]);
-    const int64_t row = (int64_t)e * H + h0 + (lane & 15);
+    const int e = __builtin_amdgcn_readfirstlane(nth_chosen(map, item / split * parts + mine));
+    const int n = list_pairs(chosen, pairs, e, list);
+    const int64_t row = (int64_t)e * H + h0;
     const uint8_t* wc[1] = {w2 + row * IB * 16};
     const uint8_t* ws[1] = {w2_s + row * IB};
-    // Columns 0..7: hi of 8 pairs; columns 8..15: lo of the same.
-    for (int p0 = 0; p0 < n_pairs; p0 += 8) {
-      const int mine = lists[wave][min(p0 + (lane & 7), n_pairs - 1)];
-      const uint16_t* a = act + ((int64_t)mine * 2 + ((lane >> 3) & 1)) * I;
+    for (int p0 = 0; p0 < n; p0 += kRows) {
+      X rows;
+#pragma unroll
+      for (int i = 0; i < kRows / 2; ++i)
+        rows.p[i] =
+            act + (int64_t)list[min(p0 + 2 * i + (lane >> 5), n - 1)] * I + (lane & 7) * 4;
       v4f_t acc[1] = {v4f_t{}};
-      few_mac<1>(wc, ws, reinterpret_cast<const uint8_t*>(a), IB, s, split, lane >> 4, acc);
+      few_stream<1>(wc, ws, [](int, int r) { return r; }, rows, IB, s, split,
+                    lds + wave * few_lds_bytes<1, X>(), acc);
+      const int c = lane & 15;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float sum = acc[0][v] + __shfl_xor(acc[0][v], 8);
-        if ((lane & 8) == 0 && p0 + (lane & 7) < n_pairs)
-          part[((int64_t)s * pairs + mine) * 16 + 4 * (lane >> 4) + v] = sum;
+        // Sum of the pieces' columns.
+        float sum = c < X::kColumns ? acc[0][v] : 0.0f;
+        sum += __shfl_xor(sum, kRows);
+        if (kPieces == 3) sum += __shfl_xor(sum, 2 * kRows);
+        if (c < kRows && p0 + c < n)
+          part[(s * pairs + list[p0 + c]) * 16 + 4 * (lane >> 4) + v] = sum;
       }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < T * 16; i += kThreads) {
+  for (int i = threadIdx.x; i < T * 16; i += blockDim.x) {
     const int t = i >> 4, r = i & 15;
     float sum = 0.0f;
     for (int j = 0; j < top_k; ++j) {
-      const int p = t * top_k + j;
-      if (chosen.ids[p] < 0) continue;
+      const int p = t * top_k + j, e = chosen[p];
+      if (e < 0) continue;
+      if (parts > 1) {
+        int rank = __popc(map[e >> 5] & ((1u << (e & 31)) - 1));
+        for (int w = 0; w < e >> 5; ++w) rank += __popc(map[w]);
+        if (rank % parts != mine) continue;
+      }
       float v = part[p * 16 + r];
       for (int s = 1; s < split; ++s) v += part[(s * pairs + p) * 16 + r];
       sum += weights[p] * v;
     }
-    const int64_t o = (int64_t)t * H + h0 + r;
-    if constexpr (kOutFp32)
-      static_cast<float*>(y)[o] = sum;
+    if (parts == 1)
+      store_y<kOutFp32>(y, (int64_t)t * H + h0 + r, sum);
     else
-      static_cast<uint16_t*>(y)[o] = (uint16_t)pack_bf16x2(sum, sum);
+      __hip_atomic_store(&partial[((int64_t)mine * T + t) * H + h0 + r], sum, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
   }
+  if (parts == 1) return;
+  // The parts go through memory as device-scope atomics, which no XCD's L2
+  // holds back, and a wave's are complete once its count of outstanding
+  // stores is zero: so the workgroup counts as arrived after its stores, and
+  // the last one reads all of them. (Ordinary stores with a release fence
+  // write back a whole L2 in every workgroup: 7 tokens, H 1056, I 544, 10
+  // experts took 56 us instead of 15.)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(&counters[blockIdx.x], 1u, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != (uint32_t)parts - 1) return;
+  for (int i = threadIdx.x; i < T * 16; i += blockDim.x) {
+    const int64_t at = (int64_t)(i >> 4) * H + h0 + (i & 15);
+    float sum = 0.0f;
+    for (int s = 0; s < parts; ++s)
+      sum += __hip_atomic_load(&partial[(int64_t)s * T * H + at], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    store_y<kOutFp32>(y, at, sum);
+  }
+}
+
+template <int kMaxXL>
+hipError_t launch_up(const UpArgs& g, const int32_t* ids, int pairs, int E, uint32_t* counters,
+                     int n_counters, hipStream_t stream) {
+  const int waves = even_waves((g.HB + kUnitBlocks - 1) / kUnitBlocks, 4);
+  const int lds = waves * few_lds_bytes<2, BfRows<kMaxXL>>();
+  hipLaunchKernelGGL((moe_up_kernel<kMaxXL>), dim3(g.I / kFewTile, pairs < E ? pairs : E),
+                     dim3(64 * waves), lds, stream, g, ids, pairs, E, pairs < E ? 1 : 0, counters,
+                     n_counters);
+  return hipGetLastError();
+}
+
+template <int kRows, int kPieces, bool kOutFp32>
+hipError_t launch_down(const float* act, const int32_t* ids, const float* weights,
+                       const uint8_t* w2, const uint8_t* w2_s, int T, int H, int I, int E,
+                       int top_k, int parts, int max_split, float* partial, uint32_t* counters,
+                       void* y, hipStream_t stream) {
+  const int pairs = T * top_k, waves = kMaxWaves;
+  const int lds = waves * few_lds_bytes<1, F32Rows<kRows, kPieces>>() + max_split * pairs * 64 +
+                  pairs * 4 + waves * pairs * 2;
+  const auto kernel = moe_down_kernel<kRows, kPieces, kOutFp32>;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3(H / kFewTile, parts), dim3(64 * waves), lds, stream, act, ids,
+                     weights, w2, w2_s, T, H, I, E, top_k, max_split, partial, counters, y);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const float* weights,
                       const void* w13, const void* w13_s, const void* w2, const void* w2_s, int T,
-                      int H, int I, int E, int top_k, bool out_fp32, void* y, uint16_t* act,
+                      int H, int I, int E, int top_k, bool out_fp32, void* y, void* workspace,
                       hipStream_t stream) {
-  const int pairs = T * top_k;
-  hipLaunchKernelGGL(moe_up_kernel, dim3(I / kFewTile, pairs < E ? pairs : E), dim3(kThreads), 0,
-                     stream, static_cast<const uint8_t*>(x), ldx, ids,
-                     static_cast<const uint8_t*>(w13), static_cast<const uint8_t*>(w13_s), pairs,
-                     H, I, E, top_k, act);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  int max_split = kWaves;
-  while (max_split > 1 && max_split * pairs > kLdsSlots) max_split /= 2;
-  const size_t lds = (size_t)max_split * pairs * 16 * sizeof(float);
-  const auto kernel = out_fp32 ? moe_down_kernel<true> : moe_down_kernel<false>;
-  err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(kernel, dim3(H / kFewTile), dim3(kThreads), lds, stream, act, ids, weights,
-                     static_cast<const uint8_t*>(w2), static_cast<const uint8_t*>(w2_s), T, H, I,
-                     E, top_k, max_split, y);
-  return hipGetLastError();
+  const auto* xb = static_cast<const uint8_t*>(x);
+  const auto* c13 = static_cast<const uint8_t*>(w13);
+  const auto* s13 = static_cast<const uint8_t*>(w13_s);
+  const auto* c2 = static_cast<const uint8_t*>(w2);
+  const auto* s2 = static_cast<const uint8_t*>(w2_s);
+  const int pairs = T * top_k, HB = H / 32, IB = I / 32;
+  // Workspace: partial sums of y, the activations, the counters.
+  auto* partial = static_cast<float*>(workspace);
+  auto* act = partial + (T > 1 ? (int64_t)kMaxParts * T * H : 0);
+  auto* counters = reinterpret_cast<uint32_t*>(act + (int64_t)pairs * I);
+  hipError_t e;
+  if (T == 1) {
+    hipLaunchKernelGGL(moe_one_up_kernel, dim3(I / 2, top_k),
+                       dim3(64 * even_waves((HB + 63) / 64, kMaxWaves)), 0, stream, xb, ids, c13,
+                       s13, HB, I, E, act);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const dim3 threads(64 * even_waves((top_k * IB + 63) / 64, kMaxWaves));
+    hipLaunchKernelGGL(out_fp32 ? moe_one_down_kernel<true> : moe_one_down_kernel<false>,
+                       dim3(H / 4), threads, 0, stream, act, ids, weights, c2, s2, H, IB, E, top_k,
+                       y);
+    return hipGetLastError();
+  }
+  const int chosen = pairs < E ? pairs : E;  // experts, at most
+  const UpArgs up = {xb, ldx, c13, s13, act, HB, I, top_k};
+  e = pairs > 6 * E ? launch_up<4>(up, ids, pairs, E, counters, H / kFewTile, stream)
+                    : launch_up<2>(up, ids, pairs, E, counters, H / kFewTile, stream);
+  if (e != hipSuccess) return e;
+  int parts = (512 + H / kFewTile - 1) / (H / kFewTile);
+  if (parts > kMaxParts) parts = kMaxParts;
+  if (parts > chosen) parts = chosen;
+  int max_split = 1;
+  while (2 * max_split * chosen <= kMaxWaves * parts && 2 * max_split * pairs <= kMaxPairs)
+    max_split *= 2;
+  if (out_fp32)
+    return launch_down<4, 3, true>(act, ids, weights, c2, s2, T, H, I, E, top_k, parts, max_split,
+                                   partial, counters, y, stream);
+  if (pairs > 4 * E)
+    return launch_down<8, 2, false>(act, ids, weights, c2, s2, T, H, I, E, top_k, parts,
+                                    max_split, partial, counters, y, stream);
+  return launch_down<4, 2, false>(act, ids, weights, c2, s2, T, H, I, E, top_k, parts, max_split,
+                                  partial, counters, y, stream);
 }
 
 }  // namespace mxfp4

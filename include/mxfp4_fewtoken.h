@@ -63,9 +63,9 @@ int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, in
 
 /* The experts of an MoE layer for T routed tokens:
  *   y[t] = sum_j weights[t, j] * W2_e (silu(Wg_e x[t]) * (Wu_e x[t])),
- *   e = ids[t, j], silu(z) = z / (1 + exp(-z)), in FP32 up to y (the
- *   activation between the two products is carried as the sum of two BF16
- *   values, 16 bits of significand).
+ *   e = ids[t, j], silu(z) = z / (1 + exp(-z)), in FP32 up to y; for
+ *   BF16 results the activation between the two products may be rounded to
+ *   16 bits of significand.
  * An id outside 0 .. E - 1 adds nothing and its weight is not read into the
  * sum (an expert that another device holds); a token with no expert here
  * gets zeros. A token may name an expert more than once.
@@ -80,7 +80,7 @@ int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, in
  *   be used by another call until this one has run
  * Requires T >= 1, 1 <= top_k <= 32, T * top_k <= 1024, H and I >= 32 and
  * % 32 == 0, H and I <= 2^20, 1 <= E <= 1024, each buffer < 2^40 bytes. */
-int mxfp4_moe_workspace(int64_t T, int64_t I, int64_t top_k, int64_t* bytes);
+int mxfp4_moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top_k, int64_t* bytes);
 int mxfp4_moe(const void* x_bf16, int64_t ldx, const void* ids, const void* weights,
               const void* W13_codes, const void* W13_scales, const void* W2_codes,
               const void* W2_scales, int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k,

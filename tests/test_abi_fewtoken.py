@@ -103,11 +103,12 @@ def test_one_row_needs_no_row_stride():
 def test_workspace_sizes():
     rc, n = mx.mxfp4_moe_route_workspace(64, 128)
     assert rc == OK and n >= 64 * 128 * 8
-    rc, n = mx.mxfp4_moe_workspace(32, 768, 8)
+    rc, n = mx.mxfp4_moe_workspace(32, 2048, 768, 8)
     assert rc == OK and n >= 32 * 8 * 768 * 4
     for args in [(0, 8), (65536, 8), (4, 0), (4, 1025)]:
         assert mx.mxfp4_moe_route_workspace(*args)[0] == EINVAL
-    for args in [(0, 32, 1), (4, 33, 1), (4, 0, 1), (4, 32, 0), (4, 32, 33), (1025, 32, 1)]:
+    for args in [(0, 64, 32, 1), (4, 64, 33, 1), (4, 64, 0, 1), (4, 64, 32, 0), (4, 64, 32, 33),
+                 (1025, 64, 32, 1), (4, 48, 32, 1), (4, 0, 32, 1), (4, (1 << 20) + 32, 32, 1)]:
         assert mx.mxfp4_moe_workspace(*args)[0] == EINVAL
 
 

@@ -297,7 +297,7 @@ def test_moe_strides_canaries_and_bits():
     big[::2, :H] = bf16_to_dev(x)
     off = lambda s: torch.cat([torch.full((1,), 255, dtype=torch.uint8, device=DEV),  # noqa: E731
                                u8_to_dev(s).flatten()])[1:].view(s.shape)
-    need = mx.moe_workspace(T, I, k).numel()
+    need = mx.moe_workspace(T, H, I, k).numel()
     wsb = torch.full((need + 256,), 99, dtype=torch.uint8, device=DEV)
     args = (big[::2, :H], torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV),
             u8_to_dev(c1), off(s1), u8_to_dev(c2), off(s2))

@@ -82,6 +82,51 @@ __device__ __forceinline__ float dot_block(u32x4_t w, float scale, const u32x4_t
   return acc;
 }
 
+// The product of a block's 32 codes with 32 FP32 activations.
+__device__ __forceinline__ float dot_block_f32(u32x4_t w, float scale, const u32x4_t (&a)[8]) {
+  float dot = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t ww = w[q];
+    const v4f_t a0 = __builtin_bit_cast(v4f_t, a[2 * q]);
+    const v4f_t a1 = __builtin_bit_cast(v4f_t, a[2 * q + 1]);
+    const f32x2_t d0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 0);
+    const f32x2_t d1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 1);
+    const f32x2_t d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 2);
+    const f32x2_t d3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 3);
+    dot = fmaf(d0[0], a0[0], dot);
+    dot = fmaf(d0[1], a0[1], dot);
+    dot = fmaf(d1[0], a0[2], dot);
+    dot = fmaf(d1[1], a0[3], dot);
+    dot = fmaf(d2[0], a1[0], dot);
+    dot = fmaf(d2[1], a1[1], dot);
+    dot = fmaf(d3[0], a1[2], dot);
+    dot = fmaf(d3[1], a1[3], dot);
+  }
+  return dot;
+}
+
+// A wave's LDS for the activations of 64 blocks of kWords 16-byte words each:
+// filled as whole lines (lane l has words l, l + 64, ...), read back a block a
+// lane. The stride is odd in words, so that no reads meet on a bank.
+template <int kWords>
+struct LaneBlocks {
+  static constexpr int kStride = (kWords | 1) * 16;
+  static constexpr int kBytes = 64 * kStride;
+  static __device__ __forceinline__ void fill(uint8_t* lds, const u32x4_t (&r)[kWords]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int at = i * 64 + lane;
+      *reinterpret_cast<u32x4_t*>(lds + at / kWords * kStride + at % kWords * 16) = r[i];
+    }
+    wave_sync();
+  }
+  static __device__ __forceinline__ u32x4_t get(const uint8_t* lds, int i) {
+    return *reinterpret_cast<const u32x4_t*>(lds + (threadIdx.x & 63) * kStride + i * 16);
+  }
+};
+
 // --------------------------------------------------- several activation rows
 // Work of a wave: units of 256 k (8 blocks) of T tiles of 16 weight rows and
 // of up to 16 activation columns. Everything is fetched as whole lines (8

@@ -26,6 +26,8 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kMaxWaves = 8;
+constexpr int kOneDownRows = 8;
+constexpr int kOneDownWaves = 7;  // 63 KiB of LDS
 constexpr int kMaxPairs = 1024;
 constexpr int kMaxExperts = 1024;
 constexpr int kMapWords = kMaxExperts / 32;
@@ -89,66 +91,69 @@ __global__ __launch_bounds__(64 * kMaxWaves) void moe_one_up_kernel(
   }
 }
 
+// Eight rows of y and not four: every workgroup reads all of the activations
+// from L2 (8 experts, top 2, 4096 x 14336: 15.8 against 19.4 us, with the
+// activations left out 14.7 us), as whole lines through the wave's LDS (a
+// block's 128 bytes a lane straight from memory: 22.3 us with four rows).
 template <bool kOutFp32>
-__global__ __launch_bounds__(64 * kMaxWaves) void moe_one_down_kernel(
+__global__ __launch_bounds__(64 * kOneDownWaves) void moe_one_down_kernel(
     const float* __restrict__ act, const int32_t* __restrict__ ids,
     const float* __restrict__ weights, const uint8_t* __restrict__ w2,
     const uint8_t* __restrict__ w2_s, int H, int IB, int E, int top_k, void* __restrict__ y) {
-  __shared__ float red[kMaxWaves * 4];
+  constexpr int R = kOneDownRows;
+  using Blocks = LaneBlocks<8>;
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ float red[kOneDownWaves * R];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const int h0 = blockIdx.x * 4;
-  float acc[4] = {};
+  uint8_t* mine = lds + wave * Blocks::kBytes;
+  const int h0 = blockIdx.x * R;
+  const int blocks = top_k * IB;
+  float acc[R / 4][4] = {};
   // Block b of pair j is the (j IB + b)-th; lanes without one, and those of
-  // an absent expert, load nothing.
-  for (int s = wave; s * 64 < top_k * IB; s += waves) {
-    const int j = (s * 64 + lane) / IB, b = s * 64 + lane - j * IB;
-    const int e = j < top_k ? ids[j] : -1;
-    if (e >= 0 && e < E) {
-      u32x4_t w[4];
-      uint32_t byte[4];
-      v4f_t a[8];
+  // an absent expert, load no weights.
+  for (int s = wave; s * 64 < blocks; s += waves) {
+    const int at = s * 64 + lane;
+    const int j = min(at, blocks - 1) / IB, b = at - j * IB;
+    const int e = ids[j];
+    const bool here = at < blocks && e >= 0 && e < E;
+    u32x4_t w[R], a[8];
+    uint32_t byte[R];
+    float weight = 0.0f;
+    if (here) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < R; ++r) {
         const int64_t row = (int64_t)e * H + h0 + r;
         w[r] = *reinterpret_cast<const u32x4_t*>(w2 + (row * IB + b) * 16);
         byte[r] = w2_s[row * IB + b];
       }
+      weight = weights[j];
+    }
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        a[q] = *reinterpret_cast<const v4f_t*>(act + ((int64_t)j * IB + b) * 32 + 4 * q);
-      const float weight = weights[j];
+    for (int q = 0; q < 8; ++q)
+      a[q] = *reinterpret_cast<const u32x4_t*>(
+          act + (int64_t)min(s * 512 + q * 64 + lane, blocks * 8 - 1) * 4);
+    wave_sync();
+    Blocks::fill(mine, a);
+    if (here) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float scale = scale_of_byte(byte[r]);
-        float dot = 0.0f;
+      for (int q = 0; q < 8; ++q) a[q] = Blocks::get(mine, q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t ww = w[r][q];
-          const f32x2_t d0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 0);
-          const f32x2_t d1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 1);
-          const f32x2_t d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 2);
-          const f32x2_t d3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ww, scale, 3);
-          dot = fmaf(d0[0], a[2 * q][0], dot);
-          dot = fmaf(d0[1], a[2 * q][1], dot);
-          dot = fmaf(d1[0], a[2 * q][2], dot);
-          dot = fmaf(d1[1], a[2 * q][3], dot);
-          dot = fmaf(d2[0], a[2 * q + 1][0], dot);
-          dot = fmaf(d2[1], a[2 * q + 1][1], dot);
-          dot = fmaf(d3[0], a[2 * q + 1][2], dot);
-          dot = fmaf(d3[1], a[2 * q + 1][3], dot);
-        }
-        acc[r] = fmaf(weight, dot, acc[r]);
-      }
+      for (int r = 0; r < R; ++r)
+        acc[r / 4][r % 4] = fmaf(weight, dot_block_f32(w[r], scale_of_byte(byte[r]), a),
+                                 acc[r / 4][r % 4]);
     }
   }
-  const float sum = sum_four_rows(acc);
-  if ((lane & 15) == 0) red[wave * 4 + (lane >> 4)] = sum;
+#pragma unroll
+  for (int r = 0; r < R; r += 4) {
+    const float sum = sum_four_rows(acc[r / 4]);
+    if ((lane & 15) == 0) red[wave * R + r + (lane >> 4)] = sum;
+  }
   __syncthreads();
-  if (threadIdx.x < 4) {
+  if (threadIdx.x < R) {
     float v = red[threadIdx.x];
-    for (int w = 1; w < waves; ++w) v += red[w * 4 + threadIdx.x];
+    for (int w = 1; w < waves; ++w) v += red[w * R + threadIdx.x];
     store_y<kOutFp32>(y, h0 + threadIdx.x, v);
   }
 }
@@ -429,9 +434,9 @@ hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const floa
                        s13, HB, I, E, act);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 threads(64 * even_waves((top_k * IB + 63) / 64, kMaxWaves));
+    const dim3 threads(64 * even_waves((top_k * IB + 63) / 64, kOneDownWaves));
     hipLaunchKernelGGL(out_fp32 ? moe_one_down_kernel<true> : moe_one_down_kernel<false>,
-                       dim3(H / 4), threads, 0, stream, act, ids, weights, c2, s2, H, IB, E, top_k,
+                       dim3(H / kOneDownRows), threads, threads.x / 64 * LaneBlocks<8>::kBytes, stream, act, ids, weights, c2, s2, H, IB, E, top_k,
                        y);
     return hipGetLastError();
   }

@@ -65,7 +65,7 @@ int mxfp4_gemv(const void* x_bf16, int64_t ldx, const void* W_codes, const void*
 
 int mxfp4_moe_route_workspace(int64_t T, int64_t E, int64_t* bytes) {
   if (!bytes || T < 1 || T > kMaxRouteT || E < 1 || E > kMaxExperts) return MXFP4_EINVAL;
-  *bytes = T * E * (int64_t)sizeof(double);
+  *bytes = mxfp4::moe_route_workspace_bytes(T, E);
   return MXFP4_OK;
 }
 

@@ -5,8 +5,14 @@
 // bits, and 64-bit sums make that independent of the summation order for
 // all practical inputs), p = exp(l - max l) / sum exp(l - max l) in FP32.
 //
-// Two kernels: the first writes the logits (one wave per token and expert),
-// the second takes one wave per token.
+// What bounds it: launches and the latency of two loads in a row; the sums
+// are 2 T E H flop of 64-bit arithmetic (33 MFMA-cycles a KiB of router),
+// the router's and x's bytes are few and come from L2 for all but the first
+// tokens.
+//
+// Few experts: one workgroup a token does it all (one launch). Otherwise the
+// logits are tiles of v_mfma_f64_16x16x4_f64 whose K is split over
+// workgroups, and the second kernel, one wave a token, adds the splits.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -15,40 +21,18 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kMaxPerLane = 16;  // 1024 experts over 64 lanes
+typedef double v4d_t __attribute__((ext_vector_type(4)));
+
+constexpr int kOneWaves = 16;        // of the one-launch kernel
+constexpr int kOneExperts = 4;       // that a wave takes at once
+constexpr int kOneMaxExperts = 256;  // LDS: 16 partial sums of each
+constexpr int kTile = 16;            // tokens and experts of an MFMA
+constexpr int kTileWaves = 8;
+constexpr int kSplits = 8;
 
 __device__ __forceinline__ double lo_bf16(uint32_t w) { return (double)__uint_as_float(w << 16); }
 __device__ __forceinline__ double hi_bf16(uint32_t w) {
   return (double)__uint_as_float(w & 0xFFFF0000u);
-}
-
-__global__ __launch_bounds__(kThreads) void route_logits_kernel(const uint8_t* __restrict__ x,
-                                                                int64_t ldx,
-                                                                const uint8_t* __restrict__ router,
-                                                                int T, int H, int E,
-                                                                double* __restrict__ logits) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int e = blockIdx.x;
-  const int t = blockIdx.y * kWaves + wave;
-  if (t >= T) return;
-  const auto* xr = reinterpret_cast<const u32x4_t*>(x + (int64_t)t * ldx * 2);
-  const auto* rr = reinterpret_cast<const u32x4_t*>(router + (int64_t)e * H * 2);
-  double sum = 0.0;
-  for (int i = lane; i < H / 8; i += 64) {
-    const u32x4_t a = xr[i], b = rr[i];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t aw = a[q], bw = b[q];
-      sum = fma(lo_bf16(aw), lo_bf16(bw), sum);
-      sum = fma(hi_bf16(aw), hi_bf16(bw), sum);
-    }
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  if (lane == 0) logits[(int64_t)t * E + e] = sum;
 }
 
 // A logit as an integer that orders as it does: NaN below everything else,
@@ -58,80 +42,282 @@ __device__ __forceinline__ int64_t order_key(double v) {
   const int64_t b = __double_as_longlong(v + 0.0);  // -0 counts as +0
   return b >= 0 ? b : (b ^ INT64_MAX);
 }
+__device__ __forceinline__ double of_order_key(int64_t k) {
+  if (k == INT64_MIN + 1) return __longlong_as_double(0x7FF8000000000000ll);
+  return __longlong_as_double(k >= 0 ? k : (k ^ INT64_MAX));
+}
 
-__global__ __launch_bounds__(64) void route_top_kernel(const double* __restrict__ logits, int E,
-                                                       int top_k, int renormalize,
+// A reduction over the wave, its result in every lane: four DPP steps within
+// 16 lanes, then the halves of 32 and of 64.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false);
+}
+template <int kCtrl>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+  return (uint64_t)dpp32<kCtrl>((uint32_t)(v >> 32)) << 32 | dpp32<kCtrl>((uint32_t)v);
+}
+template <class Op>
+__device__ __forceinline__ uint64_t wave_reduce64(uint64_t v, Op op) {
+  v = op(v, dpp64<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = op(v, dpp64<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = op(v, dpp64<0x141>(v));  // row_half_mirror
+  v = op(v, dpp64<0x140>(v));  // row_mirror
+  auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  auto hi =
+      __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+  v = op((uint64_t)hi[0] << 32 | lo[0], (uint64_t)hi[1] << 32 | lo[1]);
+  lo = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  hi = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+  return op((uint64_t)hi[0] << 32 | lo[0], (uint64_t)hi[1] << 32 | lo[1]);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  return __longlong_as_double((int64_t)wave_reduce64(
+      (uint64_t)__double_as_longlong(v), [](uint64_t a, uint64_t b) {
+        return (uint64_t)__double_as_longlong(__longlong_as_double((int64_t)a) +
+                                              __longlong_as_double((int64_t)b));
+      }));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  const auto add = [](float a, uint32_t b) { return a + __uint_as_float(b); };
+  v = add(v, dpp32<0xB1>(__float_as_uint(v)));
+  v = add(v, dpp32<0x4E>(__float_as_uint(v)));
+  v = add(v, dpp32<0x141>(__float_as_uint(v)));
+  v = add(v, dpp32<0x140>(__float_as_uint(v)));
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+__device__ __forceinline__ int64_t wave_max(int64_t v) {
+  return (int64_t)wave_reduce64((uint64_t)v, [](uint64_t a, uint64_t b) {
+    return (int64_t)a > (int64_t)b ? a : b;
+  });
+}
+
+// One wave: softmax and top k of the logits l[i] of experts 64 i + lane
+// (those from E on do not count).
+template <int kPerLane>
+__device__ __forceinline__ void choose(const double (&l)[kPerLane], int E, int top_k,
+                                       int renormalize, int32_t* __restrict__ ids,
+                                       float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  int64_t key[kPerLane];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) key[i] = i * 64 + lane < E ? order_key(l[i]) : INT64_MIN;
+  int64_t mine_key = INT64_MIN, top_key = INT64_MIN;
+  int mine_id = 0;
+  for (int j = 0; j < top_k; ++j) {
+    int64_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < kPerLane; ++i) best = key[i] > best ? key[i] : best;
+    best = wave_max(best);
+    // The lowest index that has it.
+    int at = 0;
+#pragma unroll
+    for (int i = kPerLane - 1; i >= 0; --i) {
+      const uint64_t m = __ballot(key[i] == best);
+      if (m) at = i * 64 + __ffsll((unsigned long long)m) - 1;
+    }
+    if (j == 0) top_key = best;
+    if (lane == j) {
+      mine_key = best;
+      mine_id = at;
+    }
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (at == i * 64 + lane) key[i] = INT64_MIN;
+  }
+  const double top = of_order_key(top_key);
+  float total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i)
+    if (i * 64 + lane < E) total += expf((float)(l[i] - top));
+  total = wave_sum(total);
+  const float p = lane < top_k ? expf((float)(of_order_key(mine_key) - top)) / total : 0.0f;
+  const float chosen = wave_sum(p);
+  if (lane < top_k) {
+    ids[lane] = mine_id;
+    weights[lane] = renormalize ? p / chosen : p;
+  }
+}
+
+// One launch: the waves share the token's experts, four at a time, and, with
+// few experts, parts of H; wave 0 adds the parts and chooses.
+__global__ __launch_bounds__(64 * kOneWaves) void route_one_kernel(
+    const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ router, int H, int E,
+    int top_k, int renormalize, int32_t* __restrict__ ids, float* __restrict__ weights) {
+  __shared__ double part[kOneWaves * kOneExperts > kOneMaxExperts ? kOneWaves * kOneExperts
+                                                                  : kOneMaxExperts];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int groups = (E + kOneExperts - 1) / kOneExperts;
+  const int parts = groups < kOneWaves ? kOneWaves / groups : 1;
+  const int64_t t = blockIdx.x;
+  const auto* xr = reinterpret_cast<const u32x4_t*>(x + t * ldx * 2);
+  for (int item = wave; item < groups * parts; item += kOneWaves) {
+    const int group = item / parts, p = item - group * parts;
+    double sum[kOneExperts] = {};
+    for (int i = p * 64 + lane; i < H / 8; i += parts * 64) {
+      const u32x4_t a = xr[i];
+      u32x4_t b[kOneExperts];
+#pragma unroll
+      for (int n = 0; n < kOneExperts; ++n) {
+        const int e = min(group * kOneExperts + n, E - 1);
+        b[n] = reinterpret_cast<const u32x4_t*>(router + (int64_t)e * H * 2)[i];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t aw = a[q];
+        const double a0 = lo_bf16(aw), a1 = hi_bf16(aw);
+#pragma unroll
+        for (int n = 0; n < kOneExperts; ++n) {
+          const uint32_t bw = b[n][q];
+          sum[n] = fma(a0, lo_bf16(bw), sum[n]);
+          sum[n] = fma(a1, hi_bf16(bw), sum[n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kOneExperts; ++n) sum[n] = wave_sum(sum[n]);
+    if (lane == 0) {
+#pragma unroll
+      for (int n = 0; n < kOneExperts; ++n) {
+        const int e = group * kOneExperts + n;
+        if (e < E) part[p * E + e] = sum[n];
+      }
+    }
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  double l[kOneMaxExperts / 64];
+#pragma unroll
+  for (int i = 0; i < kOneMaxExperts / 64; ++i) {
+    const int e = i * 64 + lane;
+    l[i] = 0.0;
+    if (e < E)
+      for (int p = 0; p < parts; ++p) l[i] += part[p * E + e];
+  }
+  choose(l, E, top_k, renormalize, ids + t * top_k, weights + t * top_k);
+}
+
+// Partial logits [split][T][E]: a workgroup takes 16 tokens, 16 experts and
+// every gridDim.z-th share of K. Lane l has 8 consecutive h of expert and
+// token l % 16, h group l / 16 of 32; element i of the eight feeds the i-th
+// MFMA, whose accumulator register v of lane l is (expert 4 v + l / 16, token
+// l % 16).
+__global__ __launch_bounds__(64 * kTileWaves) void route_logits_kernel(
+    const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ router, int T, int H,
+    int E, double* __restrict__ logits) {
+  __shared__ double red[kTileWaves * 256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
+  // Tokens and experts past the end re-read the last one; they are not stored.
+  const int64_t t = min(t0 + (lane & 15), T - 1), e = min(e0 + (lane & 15), E - 1);
+  const auto* xr = reinterpret_cast<const u32x4_t*>(x + t * ldx * 2);
+  const auto* rr = reinterpret_cast<const u32x4_t*>(router + e * H * 2);
+  v4d_t acc = {};
+  const int stride = kTileWaves * gridDim.z * 4;
+#pragma unroll 2
+  for (int c = (blockIdx.z * kTileWaves + wave) * 4; c < H / 8; c += stride) {
+    const int i = c + (lane >> 4);
+    const bool in = i < H / 8;
+    u32x4_t a = rr[in ? i : H / 8 - 1], b = xr[in ? i : H / 8 - 1];
+    if (!in) a = b = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t aw = a[q], bw = b[q];
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(lo_bf16(aw), lo_bf16(bw), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(hi_bf16(aw), hi_bf16(bw), acc, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) red[wave * 256 + v * 64 + lane] = acc[v];
+  __syncthreads();
+  if (threadIdx.x >= 256) return;
+  // Thread i: expert i % 16 of token i / 16.
+  const int r = threadIdx.x & 15, c = threadIdx.x >> 4;
+  const double* p = red + (r >> 2) * 64 + (r & 3) * 16 + c;
+  double sum = p[0];
+#pragma unroll
+  for (int w = 1; w < kTileWaves; ++w) sum += p[w * 256];
+  if (t0 + c < T && e0 + r < E)
+    logits[((int64_t)blockIdx.z * T + t0 + c) * E + e0 + r] = sum;
+}
+
+template <int kPerLane, int kCount>
+__global__ __launch_bounds__(64) void route_top_kernel(const double* __restrict__ logits, int T,
+                                                       int E, int top_k, int renormalize,
                                                        int32_t* __restrict__ ids,
                                                        float* __restrict__ weights) {
   const int lane = threadIdx.x;
   const int64_t t = blockIdx.x;
-  const double* l = logits + t * E;
-  int64_t key[kMaxPerLane];
-  double top = 0.0;
-  float total = 0.0f;
+  double l[kPerLane];
 #pragma unroll
-  for (int i = 0; i < kMaxPerLane; ++i) {
-    const int e = i * 64 + lane;
-    key[i] = e < E ? order_key(l[e]) : INT64_MIN;
+  for (int i = 0; i < kPerLane; ++i) {
+    double v[kCount];
+#pragma unroll
+    for (int s = 0; s < kCount; ++s)
+      v[s] = logits[((int64_t)s * T + t) * E + min(i * 64 + lane, E - 1)];
+    l[i] = v[0];
+#pragma unroll
+    for (int s = 1; s < kCount; ++s) l[i] += v[s];
   }
-  float chosen = 0.0f, mine = 0.0f;
-  int mine_id = 0;
-  for (int j = 0; j < top_k; ++j) {
-    int64_t best = INT64_MIN;
-    int at = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i * 64 + lane;
-      }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const int64_t ob = __shfl_xor((long long)best, d);
-      const int oa = __shfl_xor(at, d);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
-    if (j == 0) {
-      // The largest logit is known: the softmax's sum.
-      top = l[at];
-#pragma unroll
-      for (int i = 0; i < kMaxPerLane; ++i)
-        if (i * 64 + lane < E) total += expf((float)(l[i * 64 + lane] - top));
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d);
-    }
-    const float p = expf((float)(l[at] - top)) / total;
-    chosen += p;
-    if (lane == j) {
-      mine = p;
-      mine_id = at;
-    }
-#pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i)
-      if (at == i * 64 + lane) key[i] = INT64_MIN;
-  }
-  if (lane < top_k) {
-    ids[t * top_k + lane] = mine_id;
-    weights[t * top_k + lane] = renormalize ? mine / chosen : mine;
-  }
+  choose(l, E, top_k, renormalize, ids + t * top_k, weights + t * top_k);
+}
+
+template <int kCount>
+hipError_t launch_top(const double* logits, int T, int E, int top_k, int renormalize, int32_t* ids,
+                      float* weights, hipStream_t stream) {
+  const auto kernel = E <= 64    ? route_top_kernel<1, kCount>
+                      : E <= 128 ? route_top_kernel<2, kCount>
+                      : E <= 256 ? route_top_kernel<4, kCount>
+                                 : route_top_kernel<16, kCount>;
+  hipLaunchKernelGGL(kernel, dim3(T), dim3(64), 0, stream, logits, T, E, top_k, renormalize, ids,
+                     weights);
+  return hipGetLastError();
+}
+
+bool one_launch(int64_t T, int64_t H, int64_t E) {
+  // One workgroup a token takes E H / 64 wave instructions of 64-bit
+  // arithmetic on one CU; tokens beyond the CUs' number wait.
+  return E <= kOneMaxExperts && E * H <= 65536 && T <= 512;
+}
+
+int splits_of(int64_t T, int64_t E) {
+  // Fewer tiles than half the CUs: K is split over workgroups.
+  const int64_t tiles = ((T + kTile - 1) / kTile) * ((E + kTile - 1) / kTile);
+  return tiles < 128 ? kSplits : 1;
 }
 
 }  // namespace
 
+int64_t moe_route_workspace_bytes(int64_t T, int64_t E) {
+  return splits_of(T, E) * T * E * (int64_t)sizeof(double);
+}
+
 hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int T, int H, int E,
                             int top_k, bool renormalize, int32_t* ids, float* weights,
                             double* logits, hipStream_t stream) {
-  hipLaunchKernelGGL(route_logits_kernel, dim3(E, (T + kWaves - 1) / kWaves), dim3(kThreads), 0,
-                     stream, static_cast<const uint8_t*>(x), ldx,
-                     static_cast<const uint8_t*>(router), T, H, E, logits);
-  hipError_t e = hipGetLastError();
+  const auto* xb = static_cast<const uint8_t*>(x);
+  const auto* rb = static_cast<const uint8_t*>(router);
+  const int renorm = renormalize ? 1 : 0;
+  if (one_launch(T, H, E)) {
+    hipLaunchKernelGGL(route_one_kernel, dim3(T), dim3(64 * kOneWaves), 0, stream, xb, ldx, rb, H,
+                       E, top_k, renorm, ids, weights);
+    return hipGetLastError();
+  }
+  const int splits = splits_of(T, E);
+  hipLaunchKernelGGL(route_logits_kernel,
+                     dim3((E + kTile - 1) / kTile, (T + kTile - 1) / kTile, splits),
+                     dim3(64 * kTileWaves), 0, stream, xb, ldx, rb, T, H, E, logits);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(route_top_kernel, dim3(T), dim3(64), 0, stream, logits, E, top_k,
-                     renormalize ? 1 : 0, ids, weights);
-  return hipGetLastError();
+  return splits == 1
+             ? launch_top<1>(logits, T, E, top_k, renorm, ids, weights, stream)
+             : launch_top<kSplits>(logits, T, E, top_k, renorm, ids, weights, stream);
 }
 
 }  // namespace mxfp4

@@ -104,7 +104,7 @@ def load_library():
         pi64 = ctypes.POINTER(i64)
         lib.mxfp4_gemv.argtypes = [vp, i64, vp, vp, i64, i64, i64, i32, vp, vp]
         lib.mxfp4_gemv.restype = i32
-        lib.mxfp4_moe_route_workspace.argtypes = [i64, i64, pi64]
+        lib.mxfp4_moe_route_workspace.argtypes = [i64, i64, i64, pi64]
         lib.mxfp4_moe_route_workspace.restype = i32
         lib.mxfp4_moe_route.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp]
         lib.mxfp4_moe_route.restype = i32
@@ -212,10 +212,10 @@ def mxfp4_gemv(x_bf16, ldx, W_codes, W_scales, M, N, K, out_dtype, y, stream):
                                          stream))
 
 
-def mxfp4_moe_route_workspace(T, E):
+def mxfp4_moe_route_workspace(T, H, E):
     """(rc, bytes) of moe_route's workspace."""
     n = ctypes.c_int64(0)
-    rc = int(load_library().mxfp4_moe_route_workspace(T, E, ctypes.byref(n)))
+    rc = int(load_library().mxfp4_moe_route_workspace(T, H, E, ctypes.byref(n)))
     return rc, n.value
 
 
@@ -547,69 +547,25 @@ def gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype=N
 
 
 # ------------------------------------------------ few-token tensor helpers
-# Called once per layer and token, where the host's time counts: one pass
-# over the arguments and no repeated look-ups.
-def _rows(x, name):
-    """(rows, cols, ldx, device index) of a 2-D BF16 tensor on the current
-    device whose rows are each contiguous, ldx elements apart (a slice of a
-    larger activation)."""
-    import torch
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    dev = x.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device")
-    rows, cols = x.shape
-    ldx, step = x.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    return rows, cols, ldx, dev
+# Called once per layer and token, where the host's time counts: their checks
+# and allocations are in the _tensors extension (csrc/tensors.cpp).
+_ext = None
 
 
-def _check_on(t, name, dtype, shape, dev):
-    _check(t, name, dtype, shape)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the current device")
+def load_tensors():
+    """The built extension, loaded; raises if it has not been built."""
+    global _ext
+    if _ext is None:
+        import importlib
 
-
-def _out_code(out_dtype, out):
-    """(torch dtype, C ABI code) of an output from out_dtype and out."""
-    import torch
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype == torch.bfloat16:
-        return out_dtype, OUT_BF16
-    if out_dtype == torch.float32:
-        return out_dtype, OUT_FP32
-    raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-
-
-def _new(shape, dtype, device, stream):
-    """A tensor whose memory torch does not hand out again before `stream`
-    (None: the current one, in whose order torch works anyway) has used it."""
-    import torch
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _scratch(nbytes, workspace, device, stream):
-    """A workspace of at least nbytes: the caller's, or a new one."""
-    import torch
-    if workspace is None:
-        workspace = _new(nbytes, torch.uint8, device, stream)
-    else:
-        _check_on(workspace, "workspace", torch.uint8, workspace.shape, device.index)
-        if workspace.numel() < nbytes:
-            raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
-    return workspace
+        import torch  # noqa: F401  (the extension needs its libraries loaded)
+        load_library()
+        try:
+            _ext = importlib.import_module(__name__ + "._tensors")
+        except ImportError as e:
+            raise OSError(f"{os.path.join(_HERE, '_tensors.so')} does not load ({e}): build it "
+                          "with `python -m block_scaled_microscaling_amd.build`") from e
+    return _ext
 
 
 def gemv(x, codes, scales, out_dtype=None, out=None, stream=None):
@@ -619,29 +575,16 @@ def gemv(x, codes, scales, out_dtype=None, out=None, stream=None):
 
     out_dtype: torch.bfloat16 (default) or torch.float32.
     """
-    import torch
-    M, K, ldx, dev = _rows(x, "x")
-    if codes.dim() != 2:
-        raise ValueError("codes must be 2-D [N, K/2]")
-    N = codes.shape[0]
-    _check_on(codes, "codes", torch.uint8, (N, K // 2), dev)
-    _check_on(scales, "scales", torch.uint8, (N, K // 32), dev)
-    out_dtype, code = _out_code(out_dtype, out)
-    if out is None:
-        out = _new((M, N), out_dtype, x.device, stream)
-    else:
-        _check_on(out, "out", out_dtype, (M, N), dev)
-    rc = mxfp4_gemv(x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), M, N, K, code,
-                    out.data_ptr(), _stream_handle(stream))
-    if rc != 0:
-        raise Mxfp4Error(rc, "mxfp4_gemv")
-    return out
+    y = (_ext or load_tensors()).gemv(x, codes, scales, out_dtype, out, stream)
+    if type(y) is int:
+        raise Mxfp4Error(y, "mxfp4_gemv")
+    return y
 
 
-def moe_route_workspace(T, E):
-    """A workspace for moe_route on T tokens and E experts (uint8)."""
+def moe_route_workspace(T, H, E):
+    """A workspace for moe_route on T tokens of H and E experts (uint8)."""
     import torch
-    rc, nbytes = mxfp4_moe_route_workspace(T, E)
+    rc, nbytes = mxfp4_moe_route_workspace(T, H, E)
     if rc != 0:
         raise Mxfp4Error(rc, "mxfp4_moe_route_workspace")
     return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
@@ -657,31 +600,11 @@ def moe_route(x, router, top_k, renormalize=True, ids=None, weights=None, worksp
     lowest index first), and their softmax weights, divided by their sum
     when `renormalize` is true.
     """
-    import torch
-    T, H, ldx, dev = _rows(x, "x")
-    if router.dim() != 2:
-        raise ValueError("router must be 2-D [E, H]")
-    E = router.shape[0]
-    _check_on(router, "router", torch.bfloat16, (E, H), dev)
-    top_k = int(top_k)
-    rc, nbytes = mxfp4_moe_route_workspace(T, E)
-    if rc != 0 or top_k < 1:
-        raise Mxfp4Error(rc or -1, "mxfp4_moe_route")
-    if ids is None:
-        ids = _new((T, top_k), torch.int32, x.device, stream)
-    else:
-        _check_on(ids, "ids", torch.int32, (T, top_k), dev)
-    if weights is None:
-        weights = _new((T, top_k), torch.float32, x.device, stream)
-    else:
-        _check_on(weights, "weights", torch.float32, (T, top_k), dev)
-    ws = _scratch(nbytes, workspace, x.device, stream)
-    rc = mxfp4_moe_route(x.data_ptr(), ldx, router.data_ptr(), T, H, E, top_k,
-                         1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
-                         ws.data_ptr(), _stream_handle(stream))
-    if rc != 0:
-        raise Mxfp4Error(rc, "mxfp4_moe_route")
-    return ids, weights
+    r = (_ext or load_tensors()).moe_route(x, router, top_k, renormalize, ids, weights,
+                                               workspace, stream)
+    if type(r) is int:
+        raise Mxfp4Error(r, "mxfp4_moe_route")
+    return r
 
 
 def moe_workspace(T, H, I, top_k):
@@ -705,30 +628,8 @@ def moe(x, ids, weights, w13_codes, w13_scales, w2_codes, w2_scales, out_dtype=N
     w2_scales [E, H, I/32] (quantize of the weights as [E * rows, K]).
     out_dtype: torch.bfloat16 (default) or torch.float32.
     """
-    import torch
-    T, H, ldx, dev = _rows(x, "x")
-    if ids.dim() != 2 or w13_codes.dim() != 3 or w2_codes.dim() != 3:
-        raise ValueError("ids must be 2-D [T, top_k] and the expert weights 3-D")
-    top_k = ids.shape[1]
-    E, I = w13_codes.shape[0], w2_codes.shape[2] * 2
-    _check_on(ids, "ids", torch.int32, (T, top_k), dev)
-    _check_on(weights, "weights", torch.float32, (T, top_k), dev)
-    _check_on(w13_codes, "w13_codes", torch.uint8, (E, 2 * I, H // 2), dev)
-    _check_on(w13_scales, "w13_scales", torch.uint8, (E, 2 * I, H // 32), dev)
-    _check_on(w2_codes, "w2_codes", torch.uint8, (E, H, I // 2), dev)
-    _check_on(w2_scales, "w2_scales", torch.uint8, (E, H, I // 32), dev)
-    out_dtype, code = _out_code(out_dtype, out)
-    if out is None:
-        out = _new((T, H), out_dtype, x.device, stream)
-    else:
-        _check_on(out, "out", out_dtype, (T, H), dev)
-    rc, nbytes = mxfp4_moe_workspace(T, H, I, top_k)
-    if rc != 0:
-        raise Mxfp4Error(rc, "mxfp4_moe")
-    ws = _scratch(nbytes, workspace, x.device, stream)
-    rc = mxfp4_moe(x.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), w13_codes.data_ptr(),
-                   w13_scales.data_ptr(), w2_codes.data_ptr(), w2_scales.data_ptr(), T, H, I, E,
-                   top_k, code, out.data_ptr(), ws.data_ptr(), _stream_handle(stream))
-    if rc != 0:
-        raise Mxfp4Error(rc, "mxfp4_moe")
-    return out
+    y = (_ext or load_tensors()).moe(x, ids, weights, w13_codes, w13_scales, w2_codes,
+                                         w2_scales, out_dtype, out, workspace, stream)
+    if type(y) is int:
+        raise Mxfp4Error(y, "mxfp4_moe")
+    return y

@@ -48,6 +48,43 @@ def build(verbose=True):
     return LIB
 
 
+# The tensor layer of the few-token operators (csrc/tensors.cpp): a Python
+# extension against the installed torch, built next to the library by g++.
+TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
+TENSORS_LIB = os.path.join(HERE, "_tensors.so")
+
+
+def tensors_command(out=TENSORS_LIB):
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                                os.path.join(rocm, "include")]
+    return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-Wextra",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [
+            flag for path in includes for flag in ("-isystem", path)] + [
+            "-o", str(out), TENSORS_SRC, "-L" + HERE, "-lmxfp4", "-L" + torch_lib, "-lc10",
+            "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+
+
+def build_tensors(verbose=True):
+    """Compile the tensor layer against libmxfp4.so; raises on an error."""
+    tmp = TENSORS_LIB + ".tmp"
+    cmd = tensors_command(tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr + "\n")
+        raise subprocess.CalledProcessError(res.returncode, cmd)
+    os.replace(tmp, TENSORS_LIB)
+    return TENSORS_LIB
+
+
 # A plain C program that drives the library through include/mxfp4.h alone
 # (tests/c_abi/c_abi_check.c), built next to the library by gcc: the C ABI
 # used with no Python in the process.
@@ -149,5 +186,6 @@ def build_asan(out, verbose=False):
 
 if __name__ == "__main__":
     build()
+    build_tensors()
     build_c_check()
     build_probe()

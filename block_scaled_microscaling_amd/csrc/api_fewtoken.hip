@@ -63,19 +63,20 @@ int mxfp4_gemv(const void* x_bf16, int64_t ldx, const void* W_codes, const void*
                                           static_cast<hipStream_t>(stream)));
 }
 
-int mxfp4_moe_route_workspace(int64_t T, int64_t E, int64_t* bytes) {
+int mxfp4_moe_route_workspace(int64_t T, int64_t H, int64_t E, int64_t* bytes) {
   if (!bytes || T < 1 || T > kMaxRouteT || E < 1 || E > kMaxExperts) return MXFP4_EINVAL;
-  *bytes = mxfp4::moe_route_workspace_bytes(T, E);
+  if (H < 8 || H % 8 != 0 || H > kMaxK) return MXFP4_EINVAL;
+  *bytes = mxfp4::moe_route_workspace_bytes(T, H, E);
   return MXFP4_OK;
 }
 
 int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, int64_t T, int64_t H,
                     int64_t E, int64_t top_k, int renormalize, void* ids, void* weights,
                     void* workspace, void* stream) {
-  if (!x_bf16 || !router_bf16 || !ids || !weights || !workspace) return MXFP4_EINVAL;
+  if (!x_bf16 || !router_bf16 || !ids || !weights) return MXFP4_EINVAL;
   int64_t bytes = 0;
-  if (mxfp4_moe_route_workspace(T, E, &bytes) != MXFP4_OK) return MXFP4_EINVAL;
-  if (H < 8 || H % 8 != 0 || H > kMaxK) return MXFP4_EINVAL;
+  if (mxfp4_moe_route_workspace(T, H, E, &bytes) != MXFP4_OK) return MXFP4_EINVAL;
+  if (bytes > 0 && !workspace) return MXFP4_EINVAL;
   if (top_k < 1 || top_k > kMaxTopK || top_k > E) return MXFP4_EINVAL;
   if (renormalize != 0 && renormalize != 1) return MXFP4_EINVAL;
   if (!valid_rows(T, H, ldx)) return MXFP4_EINVAL;

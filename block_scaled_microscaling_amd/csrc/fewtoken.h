@@ -341,7 +341,7 @@ constexpr int kMoeMaxParts = 8;
 // Launchers: arguments are validated by the caller.
 hipError_t launch_gemv(const void* x, int64_t ldx, const void* codes, const void* scales, int M,
                        int N, int K, bool out_fp32, void* y, hipStream_t stream);
-int64_t moe_route_workspace_bytes(int64_t T, int64_t E);
+int64_t moe_route_workspace_bytes(int64_t T, int64_t H, int64_t E);
 hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int T, int H, int E,
                             int top_k, bool renormalize, int32_t* ids, float* weights,
                             double* logits, hipStream_t stream);

@@ -294,8 +294,8 @@ int splits_of(int64_t T, int64_t E) {
 
 }  // namespace
 
-int64_t moe_route_workspace_bytes(int64_t T, int64_t E) {
-  return splits_of(T, E) * T * E * (int64_t)sizeof(double);
+int64_t moe_route_workspace_bytes(int64_t T, int64_t H, int64_t E) {
+  return one_launch(T, H, E) ? 0 : splits_of(T, E) * T * E * (int64_t)sizeof(double);
 }
 
 hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int T, int H, int E,

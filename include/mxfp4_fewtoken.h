@@ -52,11 +52,12 @@ int mxfp4_gemv(const void* x_bf16, int64_t ldx, const void* W_codes, const void*
  * x_bf16 [T, H] as mxfp4_gemv's x; router_bf16 [E, H] BF16, 16-byte aligned
  * ids [T, top_k] int32, weights [T, top_k] FP32: 4-byte aligned
  * workspace: mxfp4_moe_route_workspace bytes, 16-byte aligned, any content;
- *   not to be used by another call until this one has run
+ *   not to be used by another call until this one has run. It is 0 bytes,
+ *   and workspace may be NULL, where the sizes need none
  * Requires 1 <= T <= 65535, H % 8 == 0, 8 <= H <= 2^24, 1 <= E <= 1024,
  * 1 <= top_k <= min(E, 32), renormalize 0 or 1. A token with NaN logits gets
  * distinct ids below E (NaN sorts last) and NaN weights. */
-int mxfp4_moe_route_workspace(int64_t T, int64_t E, int64_t* bytes);
+int mxfp4_moe_route_workspace(int64_t T, int64_t H, int64_t E, int64_t* bytes);
 int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, int64_t T,
                     int64_t H, int64_t E, int64_t top_k, int renormalize, void* ids,
                     void* weights, void* workspace, void* stream);

@@ -63,7 +63,8 @@ def test_gemv_refuses_misaligned(bad):
     dict(T=0), dict(T=65536), dict(H=0), dict(H=60), dict(H=(1 << 24) + 8), dict(E=0),
     dict(E=1025), dict(k=0), dict(k=9), dict(k=-1), dict(E=64, k=33), dict(renorm=2),
     dict(renorm=-1), dict(ldx=56), dict(ldx=68), dict(ldx=0),
-    dict(x=None), dict(router=None), dict(ids=None), dict(weights=None), dict(ws=None)])
+    dict(x=None), dict(router=None), dict(ids=None), dict(weights=None),
+    dict(ws=None, H=4096, ldx=4096, E=128)])
 def test_route_refuses(bad):
     assert route(**bad) == EINVAL
 
@@ -101,11 +102,16 @@ def test_one_row_needs_no_row_stride():
 
 
 def test_workspace_sizes():
-    rc, n = mx.mxfp4_moe_route_workspace(64, 128)
+    # A size that one launch handles needs none, and then takes NULL.
+    assert mx.mxfp4_moe_route_workspace(4, 64, 8) == (OK, 0)
+    if not mx.mxfp4_available():
+        assert route(ws=None) == EUNSUPPORTED
+    rc, n = mx.mxfp4_moe_route_workspace(64, 4096, 128)
     assert rc == OK and n >= 64 * 128 * 8
     rc, n = mx.mxfp4_moe_workspace(32, 2048, 768, 8)
     assert rc == OK and n >= 32 * 8 * 768 * 4
-    for args in [(0, 8), (65536, 8), (4, 0), (4, 1025)]:
+    for args in [(0, 64, 8), (65536, 64, 8), (4, 64, 0), (4, 64, 1025), (4, 0, 8), (4, 60, 8),
+                 (4, (1 << 24) + 8, 8)]:
         assert mx.mxfp4_moe_route_workspace(*args)[0] == EINVAL
     for args in [(0, 64, 32, 1), (4, 64, 33, 1), (4, 64, 0, 1), (4, 64, 32, 0), (4, 64, 32, 33),
                  (1025, 64, 32, 1), (4, 48, 32, 1), (4, 0, 32, 1), (4, (1 << 20) + 32, 32, 1)]:

@@ -192,7 +192,7 @@ def test_route_nan_rows_and_strides():
     wb = torch.full((T * k + 32,), 77.0, device=DEV)
     ids, w = ib[16:-16].view(T, k), wb[16:-16].view(T, k)
     mx.moe_route(xs, bf16_to_dev(r), k, ids=ids, weights=w,
-                 workspace=mx.moe_route_workspace(T, E))
+                 workspace=mx.moe_route_workspace(T, H, E))
     rows = [0, 1, 3, 4, 5]
     assert np.array_equal(ids.cpu().numpy()[rows], want_ids[rows])
     check(w[rows], want[rows], tol[rows])
@@ -419,8 +419,13 @@ def test_refusals_of_the_tensor_layer():
         mx.moe_route(x, x, 5)                      # more than there are
     with pytest.raises(mx.Mxfp4Error):
         mx.moe_route(x, x, 0)
+    many = torch.zeros((300, 64), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError):
-        mx.moe_route(x, x, 2, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+        mx.moe_route(x, many, 2, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+    with pytest.raises(TypeError):
+        mx.moe_route(x, many, 2, workspace=torch.empty(1 << 20, device=DEV))
+    with pytest.raises(TypeError):
+        mx.gemv(x, c, s, stream=0)
     ids = torch.zeros((4, 2), dtype=torch.int32, device=DEV)
     ex = (torch.zeros((2, 64, 32), dtype=torch.uint8, device=DEV),
           torch.zeros((2, 64, 2), dtype=torch.uint8, device=DEV),

@@ -95,10 +95,8 @@ int mxfp4_moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top_k, int64_t*
     return MXFP4_EINVAL;
   if (H < 32 || H % 32 != 0 || H > kMaxMoeDim || I < 32 || I % 32 != 0 || I > kMaxMoeDim)
     return MXFP4_EINVAL;
-  // The activations; with several tokens, partial sums of y and a counter per
-  // 16 of its columns.
-  *bytes = T * top_k * I * (int64_t)sizeof(float);
-  if (T > 1) *bytes += mxfp4::kMoeMaxParts * T * H * (int64_t)sizeof(float) + H / 16 * 4;
+  // The pairs' activations; with several tokens, their parts of y too.
+  *bytes = T * top_k * (I + (T > 1 ? H : 0)) * (int64_t)sizeof(float);
   return MXFP4_OK;
 }
 

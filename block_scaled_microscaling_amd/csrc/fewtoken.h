@@ -335,9 +335,6 @@ inline int even_waves(int items, int most) {
   return (items + rounds - 1) / rounds;
 }
 
-// Parts into which moe's second kernel splits the experts, at most.
-constexpr int kMoeMaxParts = 8;
-
 // Launchers: arguments are validated by the caller.
 hipError_t launch_gemv(const void* x, int64_t ldx, const void* codes, const void* scales, int M,
                        int N, int K, bool out_fp32, void* y, hipStream_t stream);

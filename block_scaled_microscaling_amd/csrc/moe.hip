@@ -29,9 +29,6 @@ constexpr int kMaxWaves = 8;
 constexpr int kOneDownRows = 8;
 constexpr int kOneDownWaves = 7;  // 63 KiB of LDS
 constexpr int kMaxPairs = 1024;
-constexpr int kMaxExperts = 1024;
-constexpr int kMapWords = kMaxExperts / 32;
-constexpr int kMaxParts = kMoeMaxParts;
 
 template <bool kOutFp32>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
@@ -176,6 +173,52 @@ __device__ __forceinline__ int list_pairs(const int32_t* ids, int pairs, int e, 
   return n;
 }
 
+// The pairs of the workgroup's expert, in LDS, and how many; e is the expert.
+// With fewer pairs than experts the grid's y counts pairs, and the first pair
+// of an expert stands for all of them; otherwise it counts experts. Every
+// wave writes the same list.
+__device__ __forceinline__ int expert_pairs(const int32_t* __restrict__ ids, int pairs, int E,
+                                            int by_pair, uint16_t* list, int& e) {
+  e = by_pair ? ids[blockIdx.y] : (int)blockIdx.y;
+  if (e < 0 || e >= E) return 0;
+  const int n = list_pairs(ids, pairs, e, list);
+  return by_pair && n > 0 && list[0] != blockIdx.y ? 0 : n;
+}
+
+// Products of two tiles of 16 weight rows, at the uniform rows row0 and row1,
+// with X's columns, K split over the workgroup's waves; the results are left
+// in LDS: part w of (tile t, row r, column c) at tile_at(t, r, c) + 256 w.
+template <class X>
+__device__ __forceinline__ void two_tiles(const uint8_t* codes, const uint8_t* scales,
+                                          int64_t row0, int64_t row1, int KB, const X& rows,
+                                          uint8_t* lds) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const uint8_t* wc[2] = {codes + row0 * KB * 16, codes + row1 * KB * 16};
+  const uint8_t* ws[2] = {scales + row0 * KB, scales + row1 * KB};
+  v4f_t acc[2] = {v4f_t{}, v4f_t{}};
+  __syncthreads();  // the last tiles' results have been read
+  few_stream<2>(wc, ws, [](int, int r) { return r; }, rows, KB, wave, waves,
+                lds + wave * few_lds_bytes<2, X>(), acc);
+  __syncthreads();
+  auto* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[(t * waves + wave) * 256 + v * 64 + lane] = acc[t][v];
+  __syncthreads();
+}
+
+__device__ __forceinline__ float tile_sum(const uint8_t* lds, int t, int r, int c) {
+  const int waves = blockDim.x >> 6;
+  const float* p = reinterpret_cast<const float*>(lds) + t * waves * 256 + (r & 3) * 64 +
+                   (r >> 2) * 16 + c;
+  float sum = p[0];
+  for (int w = 1; w < waves; ++w) sum += p[w * 256];
+  return sum;
+}
+
 struct UpArgs {
   const uint8_t* x;
   int64_t ldx;
@@ -185,230 +228,132 @@ struct UpArgs {
   int HB, I, top_k;
 };
 
-// 16 activation columns of pairs list[p0 .. p0 + 4 XL): the gate and the up
-// rows are the two tiles of few_stream, K goes round the waves.
+// Activations i0 .. i0 + 15 of the pairs list[p0 .. p0 + 4 XL).
 template <int XL>
 __device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
                                         const uint16_t* list, int p0, int n, uint8_t* lds) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
   BfRows<XL> rows;
 #pragma unroll
   for (int i = 0; i < XL; ++i) {
     const int p = list[min(p0 + 4 * i + (lane >> 4), n - 1)];
     rows.p[i] = g.x + (int64_t)(p / g.top_k) * g.ldx * 2 + (lane & 3) * 16;
   }
-  const uint8_t* wc[2] = {g.w13 + gate * g.HB * 16, g.w13 + (gate + g.I) * g.HB * 16};
-  const uint8_t* ws[2] = {g.w13_s + gate * g.HB, g.w13_s + (gate + g.I) * g.HB};
-  v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-  few_stream<2>(wc, ws, [](int, int r) { return r; }, rows, g.HB, wave, waves,
-                lds + wave * few_lds_bytes<2, BfRows<XL>>(), acc);
-  __syncthreads();
-  auto* red = reinterpret_cast<float*>(lds);
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) red[(t * waves + wave) * 256 + v * 64 + lane] = acc[t][v];
-  __syncthreads();
+  two_tiles(g.w13, g.w13_s, gate, gate + g.I, g.HB, rows, lds);
   for (int i = threadIdx.x; i < 64 * XL; i += blockDim.x) {
     const int r = i & 15, c = i >> 4;
-    const float* part = red + (r & 3) * 64 + (r >> 2) * 16 + c;
-    float gv = part[0], uv = part[waves * 256];
-    for (int w = 1; w < waves; ++w) {
-      gv += part[w * 256];
-      uv += part[(waves + w) * 256];
-    }
-    if (p0 + c < n) g.act[(int64_t)list[p0 + c] * g.I + i0 + r] = silu_mul(gv, uv);
+    if (p0 + c < n)
+      g.act[(int64_t)list[p0 + c] * g.I + i0 + r] =
+          silu_mul(tile_sum(lds, 0, r, c), tile_sum(lds, 1, r, c));
   }
-  __syncthreads();
 }
 
-// One workgroup per 16 activation columns and expert. With fewer pairs than
-// experts the grid counts pairs, and the first pair of an expert stands for
-// all of its pairs. Also clears what the second kernel counts with.
+// A workgroup takes every gridDim.x-th 16 activation columns of an expert.
 template <int kMaxXL>
-__global__ __launch_bounds__(64 * kMaxWaves) void moe_up_kernel(
-    UpArgs g, const int32_t* __restrict__ ids, int pairs, int E, int by_pair, uint32_t* counters,
-    int n_counters) {
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_up_kernel(UpArgs g,
+                                                                const int32_t* __restrict__ ids,
+                                                                int pairs, int E, int by_pair) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[kMaxPairs];
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
-  const int e = by_pair ? ids[blockIdx.y] : (int)blockIdx.y;
-  if (e < 0 || e >= E) return;
-  // Every wave writes the same list.
-  const int n = list_pairs(ids, pairs, e, list);
-  if (n == 0 || (by_pair && list[0] != blockIdx.y)) return;
-  const int i0 = blockIdx.x * kFewTile;
-  const int64_t gate = (int64_t)e * 2 * g.I + i0;
-  for (int p0 = 0; p0 < n; p0 += 4 * kMaxXL) {
-    const int left = n - p0;
-    if (left <= 4)
-      up_tile<1>(g, gate, i0, list, p0, n, lds);
-    else if (kMaxXL == 2 || left <= 8)
-      up_tile<2>(g, gate, i0, list, p0, n, lds);
-    else
-      up_tile<kMaxXL>(g, gate, i0, list, p0, n, lds);
+  int e;
+  const int n = expert_pairs(ids, pairs, E, by_pair, list, e);
+  if (n == 0) return;
+  for (int i0 = blockIdx.x * kFewTile; i0 < g.I; i0 += gridDim.x * kFewTile) {
+    const int64_t gate = (int64_t)e * 2 * g.I + i0;
+    for (int p0 = 0; p0 < n; p0 += 4 * kMaxXL) {
+      const int left = n - p0;
+      if (left <= 4)
+        up_tile<1>(g, gate, i0, list, p0, n, lds);
+      else if (kMaxXL == 2 || left <= 8)
+        up_tile<2>(g, gate, i0, list, p0, n, lds);
+      else
+        up_tile<kMaxXL>(g, gate, i0, list, p0, n, lds);
+    }
   }
 }
 
-// The chosen experts as a bit map, and the pairs' experts (-1: absent).
-__device__ __forceinline__ void read_chosen(const int32_t* __restrict__ ids, int pairs, int E,
-                                            int32_t* chosen, uint32_t* map) {
-  if (threadIdx.x < kMapWords) map[threadIdx.x] = 0;
-  __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-    const int e = ids[p];
-    const bool here = e >= 0 && e < E;
-    chosen[p] = here ? e : -1;
-    if (here) atomicOr(&map[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-}
+struct DownArgs {
+  const float* act;
+  const uint8_t* w2;
+  const uint8_t* w2_s;
+  float* part;  // [pairs][H]: W2 a of each pair
+  int H, I;
+};
 
-// The n-th chosen expert (from 0) in order of its index, of more than n.
-__device__ __forceinline__ int nth_chosen(const uint32_t* map, int n) {
-  int w = 0;
-  for (; n >= __popc(map[w]); ++w) n -= __popc(map[w]);
-  uint32_t m = map[w];
-  for (int i = 0; i < n; ++i) m &= m - 1;
-  return w * 32 + __ffs(m) - 1;
-}
-
-// One workgroup per 16 outputs h and part of the chosen experts (every
-// gridDim.y-th). Its waves take the experts in turn, with few experts also
-// the units of K; the pairs' results stay in LDS and are summed in order of
-// j. The last workgroup of an h to finish adds the parts, in order of part,
-// so y is the same on every run.
-template <int kRows, int kPieces, bool kOutFp32>
-__global__ __launch_bounds__(64 * kMaxWaves) void moe_down_kernel(
-    const float* __restrict__ act, const int32_t* __restrict__ ids,
-    const float* __restrict__ weights, const uint8_t* __restrict__ w2,
-    const uint8_t* __restrict__ w2_s, int T, int H, int I, int E, int top_k, int max_split,
-    float* __restrict__ partial, uint32_t* __restrict__ counters, void* __restrict__ y) {
-  using X = F32Rows<kRows, kPieces>;
-  extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ uint32_t map[kMapWords];
-  __shared__ uint32_t arrived;
-  const int pairs = T * top_k;
+// Outputs h0 .. h0 + 31 of the pairs list[p0 .. p0 + kRows).
+template <int kRows, int kPieces>
+__device__ __forceinline__ void down_tile(const DownArgs& g, int64_t row, int h0,
+                                          const uint16_t* list, int p0, int n, uint8_t* lds) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
-  auto* part = reinterpret_cast<float*>(lds + waves * few_lds_bytes<1, X>());  // [split][pair][16]
-  auto* chosen = reinterpret_cast<int32_t*>(part + max_split * pairs * 16);
-  auto* list = reinterpret_cast<uint16_t*>(chosen + pairs) + wave * pairs;
-  read_chosen(ids, pairs, E, chosen, map);
-  int experts = 0;
-  for (int w = 0; w < (E + 31) / 32; ++w) experts += __popc(map[w]);
-  const int parts = gridDim.y, mine = blockIdx.y;
-  const int held = (experts - mine + parts - 1) / parts;  // experts of this part
-  const int h0 = blockIdx.x * kFewTile;
-  const int IB = I / 32;
-  int split = 1;
-  while (2 * split <= max_split && 2 * split * held <= waves) split *= 2;
-  for (int item = wave; item < held * split; item += waves) {
-    const int s = item % split;
-    const int e = __builtin_amdgcn_readfirstlane(nth_chosen(map, item / split * parts + mine));
-    const int n = list_pairs(chosen, pairs, e, list);
-    const int64_t row = (int64_t)e * H + h0;
-    const uint8_t* wc[1] = {w2 + row * IB * 16};
-    const uint8_t* ws[1] = {w2_s + row * IB};
-    for (int p0 = 0; p0 < n; p0 += kRows) {
-      X rows;
+  F32Rows<kRows, kPieces> rows;
 #pragma unroll
-      for (int i = 0; i < kRows / 2; ++i)
-        rows.p[i] =
-            act + (int64_t)list[min(p0 + 2 * i + (lane >> 5), n - 1)] * I + (lane & 7) * 4;
-      v4f_t acc[1] = {v4f_t{}};
-      few_stream<1>(wc, ws, [](int, int r) { return r; }, rows, IB, s, split,
-                    lds + wave * few_lds_bytes<1, X>(), acc);
-      const int c = lane & 15;
+  for (int i = 0; i < kRows / 2; ++i)
+    rows.p[i] = g.act + (int64_t)list[min(p0 + 2 * i + (lane >> 5), n - 1)] * g.I + (lane & 7) * 4;
+  two_tiles(g.w2, g.w2_s, row, row + kFewTile, g.I / 32, rows, lds);
+  for (int i = threadIdx.x; i < 32 * kRows; i += blockDim.x) {
+    const int r = i & 31, c = i >> 5;
+    if (p0 + c >= n) continue;
+    float sum = 0.0f;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        // Sum of the pieces' columns.
-        float sum = c < X::kColumns ? acc[0][v] : 0.0f;
-        sum += __shfl_xor(sum, kRows);
-        if (kPieces == 3) sum += __shfl_xor(sum, 2 * kRows);
-        if (c < kRows && p0 + c < n)
-          part[(s * pairs + list[p0 + c]) * 16 + 4 * (lane >> 4) + v] = sum;
-      }
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < T * 16; i += blockDim.x) {
-    const int t = i >> 4, r = i & 15;
-    float sum = 0.0f;
-    for (int j = 0; j < top_k; ++j) {
-      const int p = t * top_k + j, e = chosen[p];
-      if (e < 0) continue;
-      if (parts > 1) {
-        int rank = __popc(map[e >> 5] & ((1u << (e & 31)) - 1));
-        for (int w = 0; w < e >> 5; ++w) rank += __popc(map[w]);
-        if (rank % parts != mine) continue;
-      }
-      float v = part[p * 16 + r];
-      for (int s = 1; s < split; ++s) v += part[(s * pairs + p) * 16 + r];
-      sum += weights[p] * v;
-    }
-    if (parts == 1)
-      store_y<kOutFp32>(y, (int64_t)t * H + h0 + r, sum);
-    else
-      __hip_atomic_store(&partial[((int64_t)mine * T + t) * H + h0 + r], sum, __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-  }
-  if (parts == 1) return;
-  // The parts go through memory as device-scope atomics, which no XCD's L2
-  // holds back, and a wave's are complete once its count of outstanding
-  // stores is zero: so the workgroup counts as arrived after its stores, and
-  // the last one reads all of them. (Ordinary stores with a release fence
-  // write back a whole L2 in every workgroup: 7 tokens, H 1056, I 544, 10
-  // experts took 56 us instead of 15.)
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0)
-    arrived = __hip_atomic_fetch_add(&counters[blockIdx.x], 1u, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (arrived != (uint32_t)parts - 1) return;
-  for (int i = threadIdx.x; i < T * 16; i += blockDim.x) {
-    const int64_t at = (int64_t)(i >> 4) * H + h0 + (i & 15);
-    float sum = 0.0f;
-    for (int s = 0; s < parts; ++s)
-      sum += __hip_atomic_load(&partial[(int64_t)s * T * H + at], __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-    store_y<kOutFp32>(y, at, sum);
+    for (int piece = kPieces - 1; piece >= 0; --piece)
+      sum += tile_sum(lds, r >> 4, r & 15, piece * kRows + c);
+    g.part[(int64_t)list[p0 + c] * g.H + h0 + r] = sum;
   }
 }
 
-template <int kMaxXL>
-hipError_t launch_up(const UpArgs& g, const int32_t* ids, int pairs, int E, uint32_t* counters,
-                     int n_counters, hipStream_t stream) {
-  const int waves = even_waves((g.HB + kUnitBlocks - 1) / kUnitBlocks, 4);
-  const int lds = waves * few_lds_bytes<2, BfRows<kMaxXL>>();
-  hipLaunchKernelGGL((moe_up_kernel<kMaxXL>), dim3(g.I / kFewTile, pairs < E ? pairs : E),
-                     dim3(64 * waves), lds, stream, g, ids, pairs, E, pairs < E ? 1 : 0, counters,
-                     n_counters);
-  return hipGetLastError();
+// A workgroup takes every gridDim.x-th 32 outputs of an expert.
+template <int kMaxRows, int kPieces>
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_down_kernel(DownArgs g,
+                                                                  const int32_t* __restrict__ ids,
+                                                                  int pairs, int E, int by_pair) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint16_t list[kMaxPairs];
+  int e;
+  const int n = expert_pairs(ids, pairs, E, by_pair, list, e);
+  if (n == 0) return;
+  for (int h0 = blockIdx.x * 2 * kFewTile; h0 < g.H; h0 += gridDim.x * 2 * kFewTile) {
+    const int64_t row = (int64_t)e * g.H + h0;
+    for (int p0 = 0; p0 < n; p0 += kMaxRows) {
+      if (kMaxRows > 4 && n - p0 <= 4)
+        down_tile<4, kPieces>(g, row, h0, list, p0, n, lds);
+      else
+        down_tile<kMaxRows, kPieces>(g, row, h0, list, p0, n, lds);
+    }
+  }
 }
 
-template <int kRows, int kPieces, bool kOutFp32>
-hipError_t launch_down(const float* act, const int32_t* ids, const float* weights,
-                       const uint8_t* w2, const uint8_t* w2_s, int T, int H, int I, int E,
-                       int top_k, int parts, int max_split, float* partial, uint32_t* counters,
-                       void* y, hipStream_t stream) {
-  const int pairs = T * top_k, waves = kMaxWaves;
-  const int lds = waves * few_lds_bytes<1, F32Rows<kRows, kPieces>>() + max_split * pairs * 64 +
-                  pairs * 4 + waves * pairs * 2;
-  const auto kernel = moe_down_kernel<kRows, kPieces, kOutFp32>;
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (e != hipSuccess) return e;
+// y[t] = the weighted sum of the token's parts, in order of j.
+template <bool kOutFp32>
+__global__ __launch_bounds__(256) void moe_sum_kernel(const float* __restrict__ part,
+                                                      const int32_t* __restrict__ ids,
+                                                      const float* __restrict__ weights, int H,
+                                                      int E, int top_k, void* __restrict__ y) {
+  const int h = (blockIdx.x * 256 + threadIdx.x) * 2;
+  const int64_t t = blockIdx.y;
+  if (h >= H) return;
+  float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 8
+  for (int j = 0; j < top_k; ++j) {
+    const int64_t p = t * top_k + j;
+    const int e = ids[p];
+    if (e < 0 || e >= E) continue;
+    const float2 v = *reinterpret_cast<const float2*>(part + p * H + h);
+    const float w = weights[p];
+    s0 = fmaf(w, v.x, s0);
+    s1 = fmaf(w, v.y, s1);
   }
-  hipLaunchKernelGGL(kernel, dim3(H / kFewTile, parts), dim3(64 * waves), lds, stream, act, ids,
-                     weights, w2, w2_s, T, H, I, E, top_k, max_split, partial, counters, y);
-  return hipGetLastError();
+  if constexpr (kOutFp32)
+    *reinterpret_cast<float2*>(static_cast<float*>(y) + t * H + h) = make_float2(s0, s1);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(y) + t * H + h) = pack_bf16x2(s0, s1);
+}
+
+// Workgroups along x for `tiles` tiles of each of `experts` experts: a
+// workgroup takes more than one tile once there are kGroups workgroups.
+constexpr int kGroups = 2048;
+int groups_of(int tiles, int experts) {
+  const int each = (tiles * experts + kGroups - 1) / kGroups;
+  return (tiles + each - 1) / each;
 }
 
 }  // namespace
@@ -423,10 +368,9 @@ hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const floa
   const auto* c2 = static_cast<const uint8_t*>(w2);
   const auto* s2 = static_cast<const uint8_t*>(w2_s);
   const int pairs = T * top_k, HB = H / 32, IB = I / 32;
-  // Workspace: partial sums of y, the activations, the counters.
-  auto* partial = static_cast<float*>(workspace);
-  auto* act = partial + (T > 1 ? (int64_t)kMaxParts * T * H : 0);
-  auto* counters = reinterpret_cast<uint32_t*>(act + (int64_t)pairs * I);
+  // Workspace: the activations, then, with several tokens, the pairs' parts of y.
+  auto* act = static_cast<float*>(workspace);
+  auto* part = act + (int64_t)pairs * I;
   hipError_t e;
   if (T == 1) {
     hipLaunchKernelGGL(moe_one_up_kernel, dim3(I / 2, top_k),
@@ -441,24 +385,41 @@ hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const floa
     return hipGetLastError();
   }
   const int chosen = pairs < E ? pairs : E;  // experts, at most
+  const int by_pair = pairs < E ? 1 : 0;
   const UpArgs up = {xb, ldx, c13, s13, act, HB, I, top_k};
-  e = pairs > 6 * E ? launch_up<4>(up, ids, pairs, E, counters, H / kFewTile, stream)
-                    : launch_up<2>(up, ids, pairs, E, counters, H / kFewTile, stream);
+  const dim3 up_grid(groups_of(I / kFewTile, chosen), chosen);
+  const int up_waves = even_waves((HB + kUnitBlocks - 1) / kUnitBlocks, 4);
+  if (pairs > 6 * E)
+    hipLaunchKernelGGL((moe_up_kernel<4>), up_grid, dim3(64 * up_waves),
+                       (up_waves * few_lds_bytes<2, BfRows<4>>()), stream, up, ids, pairs, E,
+                       by_pair);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<2>), up_grid, dim3(64 * up_waves),
+                       (up_waves * few_lds_bytes<2, BfRows<2>>()), stream, up, ids, pairs, E,
+                       by_pair);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
-  int parts = (512 + H / kFewTile - 1) / (H / kFewTile);
-  if (parts > kMaxParts) parts = kMaxParts;
-  if (parts > chosen) parts = chosen;
-  int max_split = 1;
-  while (2 * max_split * chosen <= kMaxWaves * parts && 2 * max_split * pairs <= kMaxPairs)
-    max_split *= 2;
+  const DownArgs down = {act, c2, s2, part, H, I};
+  const dim3 down_grid(groups_of(H / (2 * kFewTile), chosen), chosen);
+  const int down_waves = even_waves((IB + kUnitBlocks - 1) / kUnitBlocks, 4);
   if (out_fp32)
-    return launch_down<4, 3, true>(act, ids, weights, c2, s2, T, H, I, E, top_k, parts, max_split,
-                                   partial, counters, y, stream);
-  if (pairs > 4 * E)
-    return launch_down<8, 2, false>(act, ids, weights, c2, s2, T, H, I, E, top_k, parts,
-                                    max_split, partial, counters, y, stream);
-  return launch_down<4, 2, false>(act, ids, weights, c2, s2, T, H, I, E, top_k, parts, max_split,
-                                  partial, counters, y, stream);
+    hipLaunchKernelGGL((moe_down_kernel<4, 3>), down_grid, dim3(64 * down_waves),
+                       (down_waves * few_lds_bytes<2, F32Rows<4, 3>>()), stream, down, ids, pairs, E,
+                       by_pair);
+  else if (pairs > 4 * E)
+    hipLaunchKernelGGL((moe_down_kernel<8, 2>), down_grid, dim3(64 * down_waves),
+                       (down_waves * few_lds_bytes<2, F32Rows<8, 2>>()), stream, down, ids, pairs, E,
+                       by_pair);
+  else
+    hipLaunchKernelGGL((moe_down_kernel<4, 2>), down_grid, dim3(64 * down_waves),
+                       (down_waves * few_lds_bytes<2, F32Rows<4, 2>>()), stream, down, ids, pairs, E,
+                       by_pair);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(out_fp32 ? moe_sum_kernel<true> : moe_sum_kernel<false>,
+                     dim3((H / 2 + 255) / 256, T), dim3(256), 0, stream, part, ids, weights, H, E,
+                     top_k, y);
+  return hipGetLastError();
 }
 
 }  // namespace mxfp4

@@ -181,8 +181,9 @@ struct BfRows {
 // rest that FP32 holds exactly, at most 2^-9 of the value, so two pieces give
 // 16 bits of significand and three all 24 (values below 2^-100 fewer). Lane l
 // loads rows 2 i + l / 32, 4 values each.
-template <int kRows, int kPieces>
+template <int kRowCount, int kPieces>
 struct F32Rows {
+  static constexpr int kRows = kRowCount;
   static constexpr int kColumns = kRows * kPieces;
   struct Half {
     v4f_t r[kRows / 2];

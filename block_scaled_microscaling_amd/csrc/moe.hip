@@ -29,6 +29,7 @@ constexpr int kMaxWaves = 8;
 constexpr int kOneDownRows = 8;
 constexpr int kOneDownWaves = 7;  // 63 KiB of LDS
 constexpr int kMaxPairs = 1024;
+constexpr int kTileWaves = 4;  // of the kernels for several tokens
 
 template <bool kOutFp32>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
@@ -228,10 +229,10 @@ struct UpArgs {
   int HB, I, top_k;
 };
 
-// Activations i0 .. i0 + 15 of the pairs list[p0 .. p0 + 4 XL).
+// The tokens of the pairs list[p0 .. p0 + 4 XL); past the n-th, of the last.
 template <int XL>
-__device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
-                                        const uint16_t* list, int p0, int n, uint8_t* lds) {
+__device__ __forceinline__ BfRows<XL> up_rows(const UpArgs& g, const uint16_t* list, int p0,
+                                              int n) {
   const int lane = threadIdx.x & 63;
   BfRows<XL> rows;
 #pragma unroll
@@ -239,7 +240,15 @@ __device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
     const int p = list[min(p0 + 4 * i + (lane >> 4), n - 1)];
     rows.p[i] = g.x + (int64_t)(p / g.top_k) * g.ldx * 2 + (lane & 3) * 16;
   }
-  two_tiles(g.w13, g.w13_s, gate, gate + g.I, g.HB, rows, lds);
+  return rows;
+}
+
+// Activations i0 .. i0 + 15 of the pairs list[p0 .. p0 + 4 XL), K split over
+// the waves.
+template <int XL>
+__device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
+                                        const uint16_t* list, int p0, int n, uint8_t* lds) {
+  two_tiles(g.w13, g.w13_s, gate, gate + g.I, g.HB, up_rows<XL>(g, list, p0, n), lds);
   for (int i = threadIdx.x; i < 64 * XL; i += blockDim.x) {
     const int r = i & 15, c = i >> 4;
     if (p0 + c < n)
@@ -248,27 +257,53 @@ __device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
   }
 }
 
-// A workgroup takes every gridDim.x-th 16 activation columns of an expert.
-template <int kMaxXL>
-__global__ __launch_bounds__(64 * kMaxWaves) void moe_up_kernel(UpArgs g,
-                                                                const int32_t* __restrict__ ids,
-                                                                int pairs, int E, int by_pair) {
+// The same with a tile a wave, over all of H: no wave waits for another.
+template <int XL>
+__device__ __forceinline__ void up_wave(const UpArgs& g, int64_t gate, int i0,
+                                        const uint16_t* list, int p0, int n, uint8_t* lds) {
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  const BfRows<XL> rows = up_rows<XL>(g, list, p0, n);
+  const uint8_t* wc[2] = {g.w13 + gate * g.HB * 16, g.w13 + (gate + g.I) * g.HB * 16};
+  const uint8_t* ws[2] = {g.w13_s + gate * g.HB, g.w13_s + (gate + g.I) * g.HB};
+  v4f_t acc[2] = {v4f_t{}, v4f_t{}};
+  few_stream<2>(wc, ws, [](int, int r) { return r; }, rows, g.HB, 0, 1, lds, acc);
+  if (c >= 4 * XL || p0 + c >= n) return;
+  v4f_t v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = silu_mul(acc[0][i], acc[1][i]);
+  *reinterpret_cast<v4f_t*>(g.act + (int64_t)list[p0 + c] * g.I + i0 + 4 * (lane >> 4)) = v;
+}
+
+// A workgroup takes 16 activation columns of an expert, or, with kWaveTiles,
+// each of its waves does.
+template <int kMaxXL, bool kWaveTiles>
+__global__ __launch_bounds__(64 * kTileWaves) void moe_up_kernel(UpArgs g,
+                                                                 const int32_t* __restrict__ ids,
+                                                                 int pairs, int E, int by_pair) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[kMaxPairs];
   int e;
   const int n = expert_pairs(ids, pairs, E, by_pair, list, e);
-  if (n == 0) return;
-  for (int i0 = blockIdx.x * kFewTile; i0 < g.I; i0 += gridDim.x * kFewTile) {
-    const int64_t gate = (int64_t)e * 2 * g.I + i0;
-    for (int p0 = 0; p0 < n; p0 += 4 * kMaxXL) {
-      const int left = n - p0;
-      if (left <= 4)
-        up_tile<1>(g, gate, i0, list, p0, n, lds);
-      else if (kMaxXL == 2 || left <= 8)
-        up_tile<2>(g, gate, i0, list, p0, n, lds);
-      else
-        up_tile<kMaxXL>(g, gate, i0, list, p0, n, lds);
-    }
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i0 = (kWaveTiles ? blockIdx.x * kTileWaves + wave : blockIdx.x) * kFewTile;
+  if (n == 0 || i0 >= g.I) return;
+  const int64_t gate = (int64_t)e * 2 * g.I + i0;
+  uint8_t* mine = lds + wave * few_lds_bytes<2, BfRows<kMaxXL>>();
+  const auto take = [&](auto xl, int p0) {
+    constexpr int XL = decltype(xl)::value;
+    if constexpr (kWaveTiles)
+      up_wave<XL>(g, gate, i0, list, p0, n, mine);
+    else
+      up_tile<XL>(g, gate, i0, list, p0, n, lds);
+  };
+  for (int p0 = 0; p0 < n; p0 += 4 * kMaxXL) {
+    const int left = n - p0;
+    if (left <= 4)
+      take(std::integral_constant<int, 1>{}, p0);
+    else if (kMaxXL == 2 || left <= 8)
+      take(std::integral_constant<int, 2>{}, p0);
+    else
+      take(std::integral_constant<int, kMaxXL>{}, p0);
   }
 }
 
@@ -280,16 +315,25 @@ struct DownArgs {
   int H, I;
 };
 
-// Outputs h0 .. h0 + 31 of the pairs list[p0 .. p0 + kRows).
+// The activations of the pairs list[p0 .. p0 + kRows); past the n-th, of the
+// last.
+template <class X>
+__device__ __forceinline__ X down_rows(const DownArgs& g, const uint16_t* list, int p0, int n) {
+  const int lane = threadIdx.x & 63;
+  X rows;
+#pragma unroll
+  for (int i = 0; i < X::kRows / 2; ++i)
+    rows.p[i] = g.act + (int64_t)list[min(p0 + 2 * i + (lane >> 5), n - 1)] * g.I + (lane & 7) * 4;
+  return rows;
+}
+
+// Outputs h0 .. h0 + 31 of the pairs list[p0 .. p0 + kRows), K split over the
+// waves.
 template <int kRows, int kPieces>
 __device__ __forceinline__ void down_tile(const DownArgs& g, int64_t row, int h0,
                                           const uint16_t* list, int p0, int n, uint8_t* lds) {
-  const int lane = threadIdx.x & 63;
-  F32Rows<kRows, kPieces> rows;
-#pragma unroll
-  for (int i = 0; i < kRows / 2; ++i)
-    rows.p[i] = g.act + (int64_t)list[min(p0 + 2 * i + (lane >> 5), n - 1)] * g.I + (lane & 7) * 4;
-  two_tiles(g.w2, g.w2_s, row, row + kFewTile, g.I / 32, rows, lds);
+  two_tiles(g.w2, g.w2_s, row, row + kFewTile, g.I / 32,
+            down_rows<F32Rows<kRows, kPieces>>(g, list, p0, n), lds);
   for (int i = threadIdx.x; i < 32 * kRows; i += blockDim.x) {
     const int r = i & 31, c = i >> 5;
     if (p0 + c >= n) continue;
@@ -301,46 +345,93 @@ __device__ __forceinline__ void down_tile(const DownArgs& g, int64_t row, int h0
   }
 }
 
-// A workgroup takes every gridDim.x-th 32 outputs of an expert.
-template <int kMaxRows, int kPieces>
-__global__ __launch_bounds__(64 * kMaxWaves) void moe_down_kernel(DownArgs g,
-                                                                  const int32_t* __restrict__ ids,
-                                                                  int pairs, int E, int by_pair) {
+// The same with a tile a wave, over all of I.
+template <int kRows, int kPieces>
+__device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0,
+                                          const uint16_t* list, int p0, int n, uint8_t* lds) {
+  using X = F32Rows<kRows, kPieces>;
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  const int IB = g.I / 32;
+  const uint8_t* wc[2] = {g.w2 + row * IB * 16, g.w2 + (row + kFewTile) * IB * 16};
+  const uint8_t* ws[2] = {g.w2_s + row * IB, g.w2_s + (row + kFewTile) * IB};
+  v4f_t acc[2] = {v4f_t{}, v4f_t{}};
+  few_stream<2>(wc, ws, [](int, int r) { return r; }, down_rows<X>(g, list, p0, n), IB, 0, 1, lds,
+                acc);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    // The sum of the pieces' columns.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float sum = c < X::kColumns ? acc[t][i] : 0.0f;
+      sum += __shfl_xor(sum, kRows);
+      if (kPieces == 3) sum += __shfl_xor(sum, 2 * kRows);
+      acc[t][i] = sum;
+    }
+    if (c < kRows && p0 + c < n)
+      *reinterpret_cast<v4f_t*>(g.part + (int64_t)list[p0 + c] * g.H + h0 + t * kFewTile +
+                                4 * (lane >> 4)) = acc[t];
+  }
+}
+
+// A workgroup takes 32 outputs of an expert, or, with kWaveTiles, each of its
+// waves does.
+template <int kMaxRows, int kPieces, bool kWaveTiles>
+__global__ __launch_bounds__(64 * kTileWaves) void moe_down_kernel(
+    DownArgs g, const int32_t* __restrict__ ids, int pairs, int E, int by_pair) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[kMaxPairs];
   int e;
   const int n = expert_pairs(ids, pairs, E, by_pair, list, e);
-  if (n == 0) return;
-  for (int h0 = blockIdx.x * 2 * kFewTile; h0 < g.H; h0 += gridDim.x * 2 * kFewTile) {
-    const int64_t row = (int64_t)e * g.H + h0;
-    for (int p0 = 0; p0 < n; p0 += kMaxRows) {
-      if (kMaxRows > 4 && n - p0 <= 4)
-        down_tile<4, kPieces>(g, row, h0, list, p0, n, lds);
-      else
-        down_tile<kMaxRows, kPieces>(g, row, h0, list, p0, n, lds);
-    }
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int h0 = (kWaveTiles ? blockIdx.x * kTileWaves + wave : blockIdx.x) * 2 * kFewTile;
+  if (n == 0 || h0 >= g.H) return;
+  const int64_t row = (int64_t)e * g.H + h0;
+  uint8_t* mine = lds + wave * few_lds_bytes<2, F32Rows<kMaxRows, kPieces>>();
+  const auto take = [&](auto r, int p0) {
+    constexpr int kRows = decltype(r)::value;
+    if constexpr (kWaveTiles)
+      down_wave<kRows, kPieces>(g, row, h0, list, p0, n, mine);
+    else
+      down_tile<kRows, kPieces>(g, row, h0, list, p0, n, lds);
+  };
+  for (int p0 = 0; p0 < n; p0 += kMaxRows) {
+    if (kMaxRows > 4 && n - p0 <= 4)
+      take(std::integral_constant<int, 4>{}, p0);
+    else
+      take(std::integral_constant<int, kMaxRows>{}, p0);
   }
 }
 
-// y[t] = the weighted sum of the token's parts, in order of j.
+// y[t] = the weighted sum of the token's parts, in order of j. The parts are
+// loaded before it is known which count, eight at a time: an absent pair's
+// part is memory that nothing wrote, and is not added.
+constexpr int kSumThreads = 64;
+
 template <bool kOutFp32>
-__global__ __launch_bounds__(256) void moe_sum_kernel(const float* __restrict__ part,
-                                                      const int32_t* __restrict__ ids,
-                                                      const float* __restrict__ weights, int H,
-                                                      int E, int top_k, void* __restrict__ y) {
-  const int h = (blockIdx.x * 256 + threadIdx.x) * 2;
+__global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(const float* __restrict__ part,
+                                                              const int32_t* __restrict__ ids,
+                                                              const float* __restrict__ weights,
+                                                              int H, int E, int top_k,
+                                                              void* __restrict__ y) {
+  const int h = (blockIdx.x * kSumThreads + threadIdx.x) * 2;
   const int64_t t = blockIdx.y;
   if (h >= H) return;
   float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 8
-  for (int j = 0; j < top_k; ++j) {
-    const int64_t p = t * top_k + j;
-    const int e = ids[p];
-    if (e < 0 || e >= E) continue;
-    const float2 v = *reinterpret_cast<const float2*>(part + p * H + h);
-    const float w = weights[p];
-    s0 = fmaf(w, v.x, s0);
-    s1 = fmaf(w, v.y, s1);
+  for (int j0 = 0; j0 < top_k; j0 += 8) {
+    float2 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = *reinterpret_cast<const float2*>(part + (t * top_k + min(j0 + j, top_k - 1)) * H + h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t p = t * top_k + min(j0 + j, top_k - 1);
+      const int e = ids[p];
+      const float w = weights[p];
+      if (j0 + j < top_k && e >= 0 && e < E) {
+        s0 = fmaf(w, v[j].x, s0);
+        s1 = fmaf(w, v[j].y, s1);
+      }
+    }
   }
   if constexpr (kOutFp32)
     *reinterpret_cast<float2*>(static_cast<float*>(y) + t * H + h) = make_float2(s0, s1);
@@ -348,12 +439,23 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const float* __restrict__ 
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(y) + t * H + h) = pack_bf16x2(s0, s1);
 }
 
-// Workgroups along x for `tiles` tiles of each of `experts` experts: a
-// workgroup takes more than one tile once there are kGroups workgroups.
-constexpr int kGroups = 2048;
-int groups_of(int tiles, int experts) {
-  const int each = (tiles * experts + kGroups - 1) / kGroups;
-  return (tiles + each - 1) / each;
+// From here on (two waves a SIMD) each wave takes a tile and all of its K;
+// with fewer tiles K is split over a workgroup's waves. 32 tokens, 128 experts
+// of 2048 x 768 (6144 and 8192 tiles): 41 + 26 us against 46 + 33; 7 tokens,
+// 10 experts of 1056 x 544 (340 tiles): 6.9 + 6.6 us against 5.3 + 5.3.
+constexpr int64_t kManyTiles = 2048;
+
+// `tiles` tiles of each expert, of `units` units of K.
+template <class Kernel, class Args>
+hipError_t launch_tiles(Kernel kernel, int lds_per_wave, const Args& g, int64_t tiles, int64_t units,
+                        bool wave_tiles, const int32_t* ids, int pairs, int E,
+                        hipStream_t stream) {
+  const int waves = wave_tiles ? kTileWaves : even_waves((int)units, kTileWaves);
+  const dim3 grid(wave_tiles ? (tiles + kTileWaves - 1) / kTileWaves : tiles,
+                  pairs < E ? pairs : E);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds_per_wave * waves, stream, g, ids, pairs,
+                     E, pairs < E ? 1 : 0);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -384,40 +486,39 @@ hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const floa
                        y);
     return hipGetLastError();
   }
-  const int chosen = pairs < E ? pairs : E;  // experts, at most
-  const int by_pair = pairs < E ? 1 : 0;
+  const int chosen = pairs < E ? pairs : E;
   const UpArgs up = {xb, ldx, c13, s13, act, HB, I, top_k};
-  const dim3 up_grid(groups_of(I / kFewTile, chosen), chosen);
-  const int up_waves = even_waves((HB + kUnitBlocks - 1) / kUnitBlocks, 4);
+  const int64_t up_tiles = I / kFewTile, up_units = (HB + kUnitBlocks - 1) / kUnitBlocks;
+  const bool up_waves = up_tiles * chosen >= kManyTiles;
+  const auto launch_up = [&](auto kernel, int lds) {
+    return launch_tiles(kernel, lds, up, up_tiles, up_units, up_waves, ids, pairs, E, stream);
+  };
   if (pairs > 6 * E)
-    hipLaunchKernelGGL((moe_up_kernel<4>), up_grid, dim3(64 * up_waves),
-                       (up_waves * few_lds_bytes<2, BfRows<4>>()), stream, up, ids, pairs, E,
-                       by_pair);
+    e = launch_up(up_waves ? moe_up_kernel<4, true> : moe_up_kernel<4, false>,
+                  few_lds_bytes<2, BfRows<4>>());
   else
-    hipLaunchKernelGGL((moe_up_kernel<2>), up_grid, dim3(64 * up_waves),
-                       (up_waves * few_lds_bytes<2, BfRows<2>>()), stream, up, ids, pairs, E,
-                       by_pair);
-  e = hipGetLastError();
+    e = launch_up(up_waves ? moe_up_kernel<2, true> : moe_up_kernel<2, false>,
+                  few_lds_bytes<2, BfRows<2>>());
   if (e != hipSuccess) return e;
   const DownArgs down = {act, c2, s2, part, H, I};
-  const dim3 down_grid(groups_of(H / (2 * kFewTile), chosen), chosen);
-  const int down_waves = even_waves((IB + kUnitBlocks - 1) / kUnitBlocks, 4);
+  const int64_t down_tiles = H / (2 * kFewTile), down_units = (IB + kUnitBlocks - 1) / kUnitBlocks;
+  const bool down_waves = down_tiles * chosen >= kManyTiles;
+  const auto launch_down = [&](auto kernel, int lds) {
+    return launch_tiles(kernel, lds, down, down_tiles, down_units, down_waves, ids, pairs, E,
+                        stream);
+  };
   if (out_fp32)
-    hipLaunchKernelGGL((moe_down_kernel<4, 3>), down_grid, dim3(64 * down_waves),
-                       (down_waves * few_lds_bytes<2, F32Rows<4, 3>>()), stream, down, ids, pairs, E,
-                       by_pair);
+    e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>,
+                    few_lds_bytes<2, F32Rows<4, 3>>());
   else if (pairs > 4 * E)
-    hipLaunchKernelGGL((moe_down_kernel<8, 2>), down_grid, dim3(64 * down_waves),
-                       (down_waves * few_lds_bytes<2, F32Rows<8, 2>>()), stream, down, ids, pairs, E,
-                       by_pair);
+    e = launch_down(down_waves ? moe_down_kernel<8, 2, true> : moe_down_kernel<8, 2, false>,
+                    few_lds_bytes<2, F32Rows<8, 2>>());
   else
-    hipLaunchKernelGGL((moe_down_kernel<4, 2>), down_grid, dim3(64 * down_waves),
-                       (down_waves * few_lds_bytes<2, F32Rows<4, 2>>()), stream, down, ids, pairs, E,
-                       by_pair);
-  e = hipGetLastError();
+    e = launch_down(down_waves ? moe_down_kernel<4, 2, true> : moe_down_kernel<4, 2, false>,
+                    few_lds_bytes<2, F32Rows<4, 2>>());
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(out_fp32 ? moe_sum_kernel<true> : moe_sum_kernel<false>,
-                     dim3((H / 2 + 255) / 256, T), dim3(256), 0, stream, part, ids, weights, H, E,
+                     dim3((H / 2 + kSumThreads - 1) / kSumThreads, T), dim3(kSumThreads), 0, stream, part, ids, weights, H, E,
                      top_k, y);
   return hipGetLastError();
 }

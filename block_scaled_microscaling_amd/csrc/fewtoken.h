@@ -130,15 +130,17 @@ struct LaneBlocks {
 // --------------------------------------------------- several activation rows
 // Work of a wave: units of 256 k (8 blocks) of T tiles of 16 weight rows and
 // of up to 16 activation columns. Everything is fetched as whole lines (8
-// weight rows x 128 B an instruction, X's activations alike), one unit ahead
-// of its use, parked in the wave's own LDS and read back as the MFMA's
-// fragments: lane l has row l % 16's dword l / 16 of a block (8 codes) and
-// the same 8 k of activation column l % 16, so accumulator register v of
-// lane l is output (weight row 4 (l / 16) + v, column l % 16).
+// weight rows x 128 B an instruction, X's activations alike), parked in the
+// wave's own LDS and read back as the MFMA's fragments: lane l has row l %
+// 16's dword l / 16 of a block (8 codes) and the same 8 k of activation
+// column l % 16, so accumulator register v of lane l is output (weight row
+// 4 (l / 16) + v, column l % 16).
 // Loading fragments straight from the rows touches 16 to 32 lines an
-// instruction: 8 x 4096 x 14336 12.0 us against 8.6 us, 16 x 28672 x 4096
-// 20 us against 16.5-17.1 us. Two, three or four units ahead measured no
-// faster at any shape, and slower where the registers cost waves.
+// instruction: 8 x 4096 x 14336 12.0 us against 8.6 us, 16 x 8192 x 8192 12.6
+// against 10.9 us. With kAhead a unit is loaded while the last one is used;
+// without, its registers make room for more waves. Two to four units ahead
+// were no faster at any shape, nor were tiles sharing the activations'
+// fragments in registers (16 x 28672 x 4096 17.0 us, 16 x 8192 x 8192 12.1).
 constexpr int kUnitBlocks = 8;
 constexpr int kXStride = 256 + 16;  // LDS row strides: padded, so that the
 constexpr int kWStride = 128 + 16;  // fragment reads meet no bank conflicts
@@ -232,7 +234,7 @@ constexpr int few_lds_bytes() {  // per wave
 // Adds to acc the products over the units first, first + stride, ... of rows
 // row(t, 0 .. 15), counted from codes[t] and scales[t] (KB blocks a row; both
 // pointers the same in every lane, the rows' bytes within 2^32 of them).
-template <int T, class X, class Row>
+template <int T, bool kAhead, class X, class Row>
 __device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
                                            const uint8_t* const (&scales)[T], const Row& row,
                                            const X& x, int KB, int first, int stride, uint8_t* lds,
@@ -280,8 +282,9 @@ __device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
     for (int h = 0; h < 2; ++h) x.load(xr[h], u, h, KB);
   };
 
-  load(first);
+  if (kAhead) load(first);
   for (int u = first; u < units; u += stride) {
+    if (!kAhead) load(u);
     const int nb = KB - u * kUnitBlocks;
     uint64_t cs[T];
 #pragma unroll
@@ -302,7 +305,7 @@ __device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
     }
     x.park(xr[0], xl);
     const typename X::Half x1 = xr[1];
-    if (u + stride < units) load(u + stride);
+    if (kAhead && u + stride < units) load(u + stride);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (h == 1) {

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_one_kernel(
 // Several rows of x: a workgroup owns T tiles of 16 weight rows and up to 16
 // rows of x, its waves take the units of 256 k in turn, and the partial tiles
 // are summed in LDS in wave order.
-template <int T, int XL, bool kOutFp32>
+template <int T, int XL, bool kAhead, bool kOutFp32>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemv_few_kernel(
     const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ scales, int M, int N, int KB, void* __restrict__ y) {
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_few_kernel(
   for (int i = 0; i < XL; ++i)
     rows.p[i] = x + (int64_t)min(m0 + 4 * i + (lane >> 4), M - 1) * ldx * 2 + (lane & 3) * 16;
   // Rows past the end re-read the last one; they are not stored.
-  few_stream<T>(wc, ws, [&](int t, int r) { return min(kFewTile * t + r, last); }, rows, KB, wave,
+  few_stream<T, kAhead>(wc, ws, [&](int t, int r) { return min(kFewTile * t + r, last); }, rows, KB, wave,
                 waves, lds + wave * few_lds_bytes<T, BfRows<XL>>(), acc);
   __syncthreads();
   auto* red = reinterpret_cast<float*>(lds);
@@ -121,17 +121,22 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_few_kernel(
   }
 }
 
-template <int T, int XL>
+template <int T, int XL, bool kAhead>
 hipError_t launch_few(const uint8_t* x, int64_t ldx, const uint8_t* codes, const uint8_t* scales,
-                      int M, int N, int KB, int most, bool out_fp32, void* y,
-                      hipStream_t stream) {
-  const int waves = even_waves((KB + kUnitBlocks - 1) / kUnitBlocks, most);
+                      int M, int N, int KB, bool out_fp32, void* y, hipStream_t stream) {
+  const int waves = even_waves((KB + kUnitBlocks - 1) / kUnitBlocks, kMaxWaves);
   // The partial tiles (T KiB a wave) take the place of what was streamed.
   static_assert(few_lds_bytes<T, BfRows<XL>>() >= T * 1024, "");
   const int lds = waves * few_lds_bytes<T, BfRows<XL>>();
   const dim3 grid((uint32_t)(((int64_t)N + T * kFewTile - 1) / (T * kFewTile)),
                   (M + kFewTile - 1) / kFewTile);
-  const auto kernel = out_fp32 ? gemv_few_kernel<T, XL, true> : gemv_few_kernel<T, XL, false>;
+  const auto kernel = out_fp32 ? gemv_few_kernel<T, XL, kAhead, true>
+                               : gemv_few_kernel<T, XL, kAhead, false>;
+  if (kMaxWaves * few_lds_bytes<T, BfRows<XL>>() > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds, stream, x, ldx, codes, scales, M, N, KB,
                      y);
   return hipGetLastError();
@@ -156,18 +161,20 @@ hipError_t launch_gemv(const void* x, int64_t ldx, const void* codes, const void
   }
   // Two tiles a workgroup halve the reads of x from L2 but also the
   // workgroups: from 384 tiles on (1.5 a CU) they pay (5 rows x 6177 x 7968
-  // 9.0 against 9.8 us, 16 x 8192 x 8192 11.3 against 12.6), below not (8 x
-  // 4096 x 14336 10.8 against 8.6, 16 x 2048 x 2048 4.1 against 3.4). With 16
-  // rows of x and two tiles, four waves leave room for a second workgroup's
-  // LDS and registers (16 x 28672 x 4096: 17.1 against 22.1 us). Up to four
-  // rows x is small and one tile is never slower by more than 1%.
+  // 8.8 against 9.6 us, 16 x 8192 x 8192 10.9 against 13.1), below not (8 x
+  // 4096 x 14336 10.7 against 8.8, 16 x 4096 x 14336 12.5 against 10.7). Up to
+  // four rows x is small and one tile is never slower by more than 1%.
+  // Loading ahead pays where a wave has few others beside it and few
+  // registers to spend (8 x 4096 x 14336 8.8 against 9.5 us), not with two
+  // tiles or 16 rows of x (8 x 28672 x 4096 15.5 against 15.1, 16 x 28672 x
+  // 4096 17.8 against 16.8, 64 x 8192 x 2048 9.9 against 9.0).
   const int64_t tiles = (((int64_t)N + kFewTile - 1) / kFewTile) * ((M + kFewTile - 1) / kFewTile);
-  if (M <= 4) return launch_few<1, 1>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream);
+  if (M <= 4) return launch_few<1, 1, true>(xb, ldx, wc, ws, M, N, KB, out_fp32, y, stream);
   if (tiles < 384)
-    return M <= 8 ? launch_few<1, 2>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream)
-                  : launch_few<1, 4>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream);
-  return M <= 8 ? launch_few<2, 2>(xb, ldx, wc, ws, M, N, KB, 8, out_fp32, y, stream)
-                : launch_few<2, 4>(xb, ldx, wc, ws, M, N, KB, 4, out_fp32, y, stream);
+    return M <= 8 ? launch_few<1, 2, true>(xb, ldx, wc, ws, M, N, KB, out_fp32, y, stream)
+                  : launch_few<1, 4, false>(xb, ldx, wc, ws, M, N, KB, out_fp32, y, stream);
+  return M <= 8 ? launch_few<2, 2, false>(xb, ldx, wc, ws, M, N, KB, out_fp32, y, stream)
+                : launch_few<2, 4, false>(xb, ldx, wc, ws, M, N, KB, out_fp32, y, stream);
 }
 
 }  // namespace mxfp4

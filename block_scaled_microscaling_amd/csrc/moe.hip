@@ -200,7 +200,7 @@ __device__ __forceinline__ void two_tiles(const uint8_t* codes, const uint8_t* s
   const uint8_t* ws[2] = {scales + row0 * KB, scales + row1 * KB};
   v4f_t acc[2] = {v4f_t{}, v4f_t{}};
   __syncthreads();  // the last tiles' results have been read
-  few_stream<2>(wc, ws, [](int, int r) { return r; }, rows, KB, wave, waves,
+  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, rows, KB, wave, waves,
                 lds + wave * few_lds_bytes<2, X>(), acc);
   __syncthreads();
   auto* red = reinterpret_cast<float*>(lds);
@@ -266,7 +266,7 @@ __device__ __forceinline__ void up_wave(const UpArgs& g, int64_t gate, int i0,
   const uint8_t* wc[2] = {g.w13 + gate * g.HB * 16, g.w13 + (gate + g.I) * g.HB * 16};
   const uint8_t* ws[2] = {g.w13_s + gate * g.HB, g.w13_s + (gate + g.I) * g.HB};
   v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-  few_stream<2>(wc, ws, [](int, int r) { return r; }, rows, g.HB, 0, 1, lds, acc);
+  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, rows, g.HB, 0, 1, lds, acc);
   if (c >= 4 * XL || p0 + c >= n) return;
   v4f_t v;
 #pragma unroll
@@ -355,7 +355,7 @@ __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0
   const uint8_t* wc[2] = {g.w2 + row * IB * 16, g.w2 + (row + kFewTile) * IB * 16};
   const uint8_t* ws[2] = {g.w2_s + row * IB, g.w2_s + (row + kFewTile) * IB};
   v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-  few_stream<2>(wc, ws, [](int, int r) { return r; }, down_rows<X>(g, list, p0, n), IB, 0, 1, lds,
+  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, down_rows<X>(g, list, p0, n), IB, 0, 1, lds,
                 acc);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {

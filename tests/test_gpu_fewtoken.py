@@ -61,6 +61,9 @@ def test_gemv_decodes_every_code_and_scale_exactly():
     (1, 1, 32), (1, 16, 256), (1, 17, 32), (2, 15, 64), (3, 33, 96), (1, 1000, 224),
     (5, 48, 288), (8, 257, 2048), (15, 31, 4128), (16, 16, 512), (17, 40, 1056), (33, 65, 736),
     (48, 64, 1024), (64, 96, 544), (65, 19, 320), (130, 35, 96), (1, 4096, 8192), (7, 512, 14336),
+    # Enough tiles for two a workgroup; one row over many rounds of K.
+    (3, 5000, 352), (5, 6177, 736), (16, 6200, 544), (40, 4001, 96), (2, 24, 32), (1, 9, 33024),
+    (6, 40, 33024),
 ])
 def test_gemv_matches_the_oracle(M, N, K, out):
     announce(f"gemv {M}x{N}x{K} {out}")
@@ -83,6 +86,18 @@ def test_gemv_on_quantized_weights_of_every_magnitude():
     x = bf16_matrix((M, K), ("normal", 0.01, 0.0, 1.0), 5)
     got = mx.gemv(bf16_to_dev(x), codes, scales, out_dtype=torch.float32)
     check(got, *fewtoken.gemv(x, codes.cpu().numpy(), scales.cpu().numpy()))
+
+
+@pytest.mark.parametrize("M", [1, 2, 20])
+def test_gemv_subnormal_activations(M):
+    """BF16 subnormals of x against weights of up to 2^127: nothing counts as
+    zero before the product."""
+    announce(f"gemv subnormal x, {M} rows")
+    N, K = 48, 288
+    x = np.random.default_rng(M).integers(1, 128, size=(M, K)).astype(np.uint16)
+    codes, scales = random_codes(N, K, 1), np.full((N, K // 32), 252, np.uint8)
+    got = mx.gemv(bf16_to_dev(x), u8_to_dev(codes), u8_to_dev(scales), out_dtype=torch.float32)
+    check(got, *fewtoken.gemv(x, codes, scales))
 
 
 def test_gemv_strided_rows_canaries_and_unaligned_scales():
@@ -235,6 +250,10 @@ def run_moe(x, ids, w, ex, **kw):
     (16, 256, 512, 40, 6, 0.5), (17, 160, 288, 1, 1, 0.0), (33, 64, 32, 6, 4, 0.1),
     (64, 128, 96, 128, 8, 0.0), (32, 96, 128, 1024, 32, 0.0), (1024, 32, 64, 3, 1, 0.2),
     (1, 512, 4096, 2, 2, 0.0), (3, 4096, 32, 5, 2, 0.0),
+    # Enough tiles for one a wave: many pairs an expert; fewer pairs than
+    # experts, and tiles that fill no workgroup.
+    (128, 1024, 512, 64, 8, 0.1), (16, 288, 288, 1000, 16, 0.2), (2, 160, 1056, 9, 9, 0.3),
+    (1, 96, 224, 40, 32, 0.5),
 ])
 def test_moe_matches_the_oracle(T, H, I, E, k, absent, out):
     announce(f"moe T{T} H{H} I{I} E{E} k{k} absent {absent} {out}")

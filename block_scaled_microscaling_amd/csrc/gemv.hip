@@ -16,6 +16,19 @@ namespace {
 
 constexpr int kMaxWaves = 8;
 
+// Workgroups along N: a grid's extent counts threads in 32 bits, so rows of
+// kGridX workgroups are stacked along z.
+constexpr int64_t kGridX = 1 << 20;
+
+__device__ __forceinline__ int64_t block_n() {
+  return (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+}
+
+dim3 grid_n(int64_t blocks, int y) {
+  return blocks <= kGridX ? dim3((uint32_t)blocks, y)
+                          : dim3((uint32_t)kGridX, y, (uint32_t)((blocks + kGridX - 1) / kGridX));
+}
+
 template <bool kOutFp32>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
   if constexpr (kOutFp32)
@@ -38,7 +51,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_one_kernel(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * kOneRows;
+  const int64_t n0 = block_n() * kOneRows;
+  if (n0 >= N) return;
   float acc[kOneRows] = {};
   for (int s = wave; s * 64 < KB; s += waves) {
     const bool in = s * 64 + lane < KB;
@@ -83,7 +97,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_few_kernel(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * (T * kFewTile);
+  const int64_t n0 = block_n() * (T * kFewTile);
+  if (n0 >= N) return;
   const int m0 = blockIdx.y * kFewTile;
   const int last = (int)min((int64_t)N - 1 - n0, (int64_t)(T * kFewTile - 1));
   const uint8_t* wc[T];
@@ -128,8 +143,8 @@ hipError_t launch_few(const uint8_t* x, int64_t ldx, const uint8_t* codes, const
   // The partial tiles (T KiB a wave) take the place of what was streamed.
   static_assert(few_lds_bytes<T, BfRows<XL>>() >= T * 1024, "");
   const int lds = waves * few_lds_bytes<T, BfRows<XL>>();
-  const dim3 grid((uint32_t)(((int64_t)N + T * kFewTile - 1) / (T * kFewTile)),
-                  (M + kFewTile - 1) / kFewTile);
+  const dim3 grid = grid_n(((int64_t)N + T * kFewTile - 1) / (T * kFewTile),
+                           (M + kFewTile - 1) / kFewTile);
   const auto kernel = out_fp32 ? gemv_few_kernel<T, XL, kAhead, true>
                                : gemv_few_kernel<T, XL, kAhead, false>;
   if (kMaxWaves * few_lds_bytes<T, BfRows<XL>>() > 65536) {
@@ -151,7 +166,7 @@ hipError_t launch_gemv(const void* x, int64_t ldx, const void* codes, const void
   const auto* ws = static_cast<const uint8_t*>(scales);
   const int KB = K / 32;
   if (M == 1) {
-    const dim3 grid((uint32_t)(((int64_t)N + kOneRows - 1) / kOneRows));
+    const dim3 grid = grid_n(((int64_t)N + kOneRows - 1) / kOneRows, 1);
     const dim3 threads(64 * even_waves((KB + 63) / 64, kMaxWaves));
     if (out_fp32)
       hipLaunchKernelGGL((gemv_one_kernel<true>), grid, threads, 0, stream, xb, wc, ws, N, KB, y);

@@ -38,7 +38,7 @@ extern "C" {
  * y [M, N] row-major, BF16 (round to nearest even) or FP32: 4-byte aligned
  * Requires 1 <= M <= 1048560, 1 <= N <= 2^31 - 1, K >= 32, K % 32 == 0,
  * K <= 2^24, each buffer < 2^40 bytes; any M and N, odd ones included. W is
- * read once per 64 rows of x: with many rows quantize them and run
+ * read once per 16 rows of x: with many rows quantize them and run
  * mxfp4_gemm. */
 int mxfp4_gemv(const void* x_bf16, int64_t ldx, const void* W_codes, const void* W_scales,
                int64_t M, int64_t N, int64_t K, int out_dtype, void* y, void* stream);

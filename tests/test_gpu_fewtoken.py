@@ -155,6 +155,22 @@ def test_gemv_past_2_32_bytes():
     check(got[:, rows], want, tol)
 
 
+def test_gemv_with_more_rows_than_a_grid_has_threads():
+    """300 million weight rows: more than 2^32 threads."""
+    announce("gemv of 3e8 rows")
+    N, K = 300_000_001, 32
+    codes = device_random_bytes((N, K // 2), 8)
+    scales = device_random_bytes((N, 1), 9, lo=117, hi=137)
+    x = device_normal_bf16((1, K), 10)
+    got = mx.gemv(x, codes, scales)
+    block = 4 << 20                            # rows of a grid's x extent
+    rows = torch.tensor([0, 3, block - 1, block, 7 * block + 5, 71 * block - 1, 71 * block, N - 2,
+                         N - 1], device=DEV)
+    want, tol = fewtoken.gemv(x.view(torch.int16).cpu().numpy().view(np.uint16),
+                              codes[rows].cpu().numpy(), scales[rows].cpu().numpy())
+    check(got[:, rows], want, tol)
+
+
 # ------------------------------------------------------------------ router
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("T,H,E,k", [
@@ -329,6 +345,19 @@ def test_moe_strides_canaries_and_bits():
         assert torch.all(wsb[:128] == 99) and torch.all(wsb[128 + need:] == 99)
         for _ in range(3):
             assert torch.equal(mx.moe(*args, out_dtype=dt), out)
+
+
+@pytest.mark.parametrize("T,k", [(1, 6), (3, 4), (64, 6)])
+def test_moe_workspace_may_hold_anything(T, k):
+    """A workspace of NaN, and absent experts whose part of it nothing writes."""
+    announce(f"moe with a workspace of NaN, {T} tokens")
+    H, I, E = 512, 288, 48
+    x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 1)
+    ids, w = choices(T, E, k, 2, 0.4)
+    ex = experts(E, H, I, 3)
+    ws = torch.full((mx.moe_workspace(T, H, I, k).numel(),), 255, dtype=torch.uint8, device=DEV)
+    for dt in (torch.float32, torch.bfloat16):
+        check(run_moe(x, ids, w, ex, out_dtype=dt, workspace=ws), *fewtoken.moe(x, ids, w, *ex))
 
 
 def test_moe_expert_weights_past_2_32_bytes():

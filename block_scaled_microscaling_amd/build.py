@@ -68,7 +68,7 @@ def tensors_command(out=TENSORS_LIB):
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [
             flag for path in includes for flag in ("-isystem", path)] + [
             "-o", str(out), TENSORS_SRC, "-L" + HERE, "-lmxfp4", "-L" + torch_lib, "-lc10",
-            "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+            "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 def build_tensors(verbose=True):

@@ -145,6 +145,7 @@ __device__ __forceinline__ void choose(const double (&l)[kPerLane], int E, int t
 
 // One launch: the waves share the token's experts, four at a time, and, with
 // few experts, parts of H; wave 0 adds the parts and chooses.
+template <int kPerLane>
 __global__ __launch_bounds__(64 * kOneWaves) void route_one_kernel(
     const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ router, int H, int E,
     int top_k, int renormalize, int32_t* __restrict__ ids, float* __restrict__ weights) {
@@ -191,9 +192,9 @@ __global__ __launch_bounds__(64 * kOneWaves) void route_one_kernel(
   }
   __syncthreads();
   if (wave != 0) return;
-  double l[kOneMaxExperts / 64];
+  double l[kPerLane];
 #pragma unroll
-  for (int i = 0; i < kOneMaxExperts / 64; ++i) {
+  for (int i = 0; i < kPerLane; ++i) {
     const int e = i * 64 + lane;
     l[i] = 0.0;
     if (e < E)
@@ -305,8 +306,9 @@ hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int 
   const auto* rb = static_cast<const uint8_t*>(router);
   const int renorm = renormalize ? 1 : 0;
   if (one_launch(T, H, E)) {
-    hipLaunchKernelGGL(route_one_kernel, dim3(T), dim3(64 * kOneWaves), 0, stream, xb, ldx, rb, H,
-                       E, top_k, renorm, ids, weights);
+    hipLaunchKernelGGL(E <= 64 ? route_one_kernel<1> : route_one_kernel<4>, dim3(T),
+                       dim3(64 * kOneWaves), 0, stream, xb, ldx, rb, H, E, top_k, renorm, ids,
+                       weights);
     return hipGetLastError();
   }
   const int splits = splits_of(T, E);

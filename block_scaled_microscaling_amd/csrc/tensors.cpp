@@ -11,6 +11,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
+#include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -100,7 +102,7 @@ struct Stream {
   // Memory that torch does not hand out again before a given stream (the
   // current one's order torch keeps anyway) has used it.
   at::Tensor empty(at::IntArrayRef shape, const at::Tensor& like, at::ScalarType dtype) const {
-    at::Tensor t = at::empty(shape, like.options().dtype(dtype));
+    at::Tensor t = at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
     if (given) t.record_stream(*given);
     return t;
   }
@@ -156,17 +158,38 @@ at::ScalarType out_type(PyObject* out_dtype, PyObject* out) {
 
 int out_code(at::ScalarType t) { return t == at::kFloat ? MXFP4_OUT_FP32 : MXFP4_OUT_BF16; }
 
-// A workspace of at least `bytes`: the caller's, or a new one.
-at::Tensor workspace(PyObject* o, int64_t bytes, const Rows& x, const Stream& stream) {
-  if (o == Py_None) return stream.empty({bytes}, x.t, at::kByte);
-  const at::Tensor& t = tensor(o, "workspace");
-  check_dtype(t, "workspace", at::kByte);
-  TORCH_CHECK_VALUE(t.is_cuda(), "workspace must be a device tensor");
-  TORCH_CHECK_VALUE(t.is_contiguous(), "workspace must be contiguous (row-major)");
-  TORCH_CHECK_VALUE(t.get_device() == x.device, "workspace must be on the current device");
-  TORCH_CHECK_VALUE(t.numel() >= bytes, "workspace must hold ", bytes, " bytes, got ", t.numel());
-  return t;
-}
+// A workspace of at least `bytes`: the caller's, or memory from torch's
+// allocator that belongs to the call's stream, so that it may be given back
+// once the call has been enqueued.
+class Workspace {
+ public:
+  Workspace(PyObject* o, int64_t bytes, const Rows& x, const Stream& stream) {
+    if (o == Py_None) {
+      if (bytes > 0)
+        own_ = c10::hip::HIPCachingAllocator::raw_alloc_with_stream(
+            bytes, static_cast<hipStream_t>(stream.handle));
+      return;
+    }
+    const at::Tensor& t = tensor(o, "workspace");
+    check_dtype(t, "workspace", at::kByte);
+    TORCH_CHECK_VALUE(t.is_cuda(), "workspace must be a device tensor");
+    TORCH_CHECK_VALUE(t.is_contiguous(), "workspace must be contiguous (row-major)");
+    TORCH_CHECK_VALUE(t.get_device() == x.device, "workspace must be on the current device");
+    TORCH_CHECK_VALUE(t.numel() >= bytes, "workspace must hold ", bytes, " bytes, got ",
+                      t.numel());
+    given_ = t.data_ptr();
+  }
+  ~Workspace() {
+    if (own_) c10::hip::HIPCachingAllocator::raw_delete(own_);
+  }
+  Workspace(const Workspace&) = delete;
+  Workspace& operator=(const Workspace&) = delete;
+  void* ptr() const { return own_ ? own_ : given_; }
+
+ private:
+  void* own_ = nullptr;
+  void* given_ = nullptr;
+};
 
 void need(Py_ssize_t got, Py_ssize_t want) {
   TORCH_CHECK_TYPE(got == want, "expected ", want, " arguments, got ", got);
@@ -210,12 +233,10 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Stream stream = stream_of(a[7], x.device);
   Output ids = output(a[4], "ids", {T, k}, at::kInt, x, stream);
   Output weights = output(a[5], "weights", {T, k}, at::kFloat, x, stream);
-  at::Tensor ws;
-  if (bytes > 0 || a[6] != Py_None) ws = workspace(a[6], bytes, x, stream);
+  const Workspace ws(a[6], bytes, x, stream);
   Py_BEGIN_ALLOW_THREADS;
   rc = mxfp4_moe_route(x.t.const_data_ptr(), x.ld, router.const_data_ptr(), T, H, E, k,
-                       renormalize, ids.t.data_ptr(), weights.t.data_ptr(),
-                       bytes > 0 ? ws.data_ptr() : nullptr,
+                       renormalize, ids.t.data_ptr(), weights.t.data_ptr(), ws.ptr(),
                        stream.handle);
   Py_END_ALLOW_THREADS;
   if (rc) return PyLong_FromLong(rc);
@@ -249,12 +270,12 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (rc) return PyLong_FromLong(rc);
   const Stream stream = stream_of(a[10], x.device);
   Output y = output(a[8], "out", {T, H}, type, x, stream);
-  const at::Tensor ws = workspace(a[9], bytes, x, stream);
+  const Workspace ws(a[9], bytes, x, stream);
   Py_BEGIN_ALLOW_THREADS;
   rc = mxfp4_moe(x.t.const_data_ptr(), x.ld, ids.const_data_ptr(), weights.const_data_ptr(),
                  c13.const_data_ptr(), s13.const_data_ptr(), c2.const_data_ptr(),
                  s2.const_data_ptr(), T, H, I, E, k, out_code(type), y.t.data_ptr(),
-                 ws.data_ptr(), stream.handle);
+                 ws.ptr(), stream.handle);
   Py_END_ALLOW_THREADS;
   return rc ? PyLong_FromLong(rc) : y.result();
   END_HANDLE_TH_ERRORS

@@ -5,6 +5,9 @@ Tolerances are the oracle's (oracle/fewtoken.py): the roundings that FP32
 sums of exact products can take, and half a step of a BF16 result.
 """
 
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -444,6 +447,22 @@ def test_layer_captured_replays_equal_eager(T):
         torch.cuda.synchronize()
         assert torch.equal(y, want), f"replay {i}"
         _ = (inp.float() * 2).sum().item()
+
+
+@pytest.mark.parametrize("tokens", [1, 5])
+def test_example_of_a_decode_step(tokens):
+    """examples/moe_decode_step.py: projection, router and experts together,
+    eagerly and as a graph. Its result is BF16 and passes three roundings of
+    2^-8, each of a value no larger than the output's range."""
+    announce(f"example of a decode step, {tokens} tokens")
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "moe_decode_step.py")
+    spec = importlib.util.spec_from_file_location("moe_decode_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    error = example.main(["--tokens", str(tokens), "--hidden", "256", "--inter", "96",
+                          "--experts", "12", "--top-k", "3", "--steps", "5"])
+    assert error < 3 * 2.0 ** -8
 
 
 def test_refusals_of_the_tensor_layer():

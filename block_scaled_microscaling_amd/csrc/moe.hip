@@ -1,5 +1,5 @@
 // The experts of a mixture-of-experts layer for a few routed tokens, MXFP4
-// weights, in two kernels.
+// weights.
 //
 // Mathematics, for pair p = t top_k + j with expert e = ids[p]:
 //   a[p, i] = silu(sum_h Wg_e[i, h] x[t, h]) * (sum_h Wu_e[i, h] x[t, h])
@@ -12,11 +12,12 @@
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
 // once: HBM.
 //
-// One token: as gemv's one-row kernel. The first kernel's workgroup has two
-// gate and two up rows of a pair's expert; the second's four rows of y, over
-// the blocks of all its experts in a row, so the sum over j needs no other
-// workgroup. Several tokens: an expert's weights are read once for all its
-// pairs, by few_stream.
+// Few pairs: as gemv's one-row kernel, in two launches. The first kernel's
+// workgroup has two gate and two up rows of a pair's expert; the second's
+// eight rows of a token's y, over the blocks of all its experts one after the
+// other, so the sum over j needs no other workgroup. Many pairs: an expert's
+// weights are read once for all its pairs, by few_stream, and a third launch
+// sums the pairs' parts of y.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,8 +27,8 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kMaxWaves = 8;
-constexpr int kOneDownRows = 8;
-constexpr int kOneDownWaves = 7;  // 63 KiB of LDS
+constexpr int kPairDownRows = 8;
+constexpr int kPairDownWaves = 7;  // 63 KiB of LDS
 constexpr int kMaxPairs = 1024;
 constexpr int kTileWaves = 4;  // of the kernels for several tokens
 
@@ -41,17 +42,18 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// --------------------------------------------------------------- one token
-__global__ __launch_bounds__(64 * kMaxWaves) void moe_one_up_kernel(
-    const uint8_t* __restrict__ x, const int32_t* __restrict__ ids,
+// --------------------------------------------------------------- by pairs
+__global__ __launch_bounds__(64 * kMaxWaves) void moe_pair_up_kernel(
+    const uint8_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ w13, const uint8_t* __restrict__ w13_s, int HB, int I, int E,
-    float* __restrict__ act) {
+    int top_k, float* __restrict__ act) {
   __shared__ float red[kMaxWaves * 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int e = ids[blockIdx.y];
   if (e < 0 || e >= E) return;
+  x += blockIdx.y / top_k * ldx * 2;
   const int64_t gate = (int64_t)e * 2 * I + 2 * blockIdx.x;
   const int64_t row[4] = {gate, gate + 1, gate + I, gate + I + 1};
   float acc[4] = {};
@@ -94,20 +96,24 @@ __global__ __launch_bounds__(64 * kMaxWaves) void moe_one_up_kernel(
 // activations left out 14.7 us), as whole lines through the wave's LDS (a
 // block's 128 bytes a lane straight from memory: 22.3 us with four rows).
 template <bool kOutFp32>
-__global__ __launch_bounds__(64 * kOneDownWaves) void moe_one_down_kernel(
+__global__ __launch_bounds__(64 * kPairDownWaves) void moe_pair_down_kernel(
     const float* __restrict__ act, const int32_t* __restrict__ ids,
     const float* __restrict__ weights, const uint8_t* __restrict__ w2,
     const uint8_t* __restrict__ w2_s, int H, int IB, int E, int top_k, void* __restrict__ y) {
-  constexpr int R = kOneDownRows;
+  constexpr int R = kPairDownRows;
   using Blocks = LaneBlocks<8>;
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ float red[kOneDownWaves * R];
+  __shared__ float red[kPairDownWaves * R];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   uint8_t* mine = lds + wave * Blocks::kBytes;
   const int h0 = blockIdx.x * R;
   const int blocks = top_k * IB;
+  const int64_t t = blockIdx.y;
+  act += t * blocks * 32;
+  ids += t * top_k;
+  weights += t * top_k;
   float acc[R / 4][4] = {};
   // Block b of pair j is the (j IB + b)-th; lanes without one, and those of
   // an absent expert, load no weights.
@@ -152,11 +158,11 @@ __global__ __launch_bounds__(64 * kOneDownWaves) void moe_one_down_kernel(
   if (threadIdx.x < R) {
     float v = red[threadIdx.x];
     for (int w = 1; w < waves; ++w) v += red[w * R + threadIdx.x];
-    store_y<kOutFp32>(y, h0 + threadIdx.x, v);
+    store_y<kOutFp32>(y, t * H + h0 + threadIdx.x, v);
   }
 }
 
-// ------------------------------------------------------------ several tokens
+// -------------------------------------------------------------- by experts
 // A wave writes the pairs of expert e in ascending order; returns how many.
 __device__ __forceinline__ int list_pairs(const int32_t* ids, int pairs, int e, uint16_t* list) {
   const int lane = threadIdx.x & 63;
@@ -458,41 +464,61 @@ hipError_t launch_tiles(Kernel kernel, int lds_per_wave, const Args& g, int64_t 
   return hipGetLastError();
 }
 
-}  // namespace
+// Whether every pair reads its expert's weights for itself. One token's
+// experts differ anyway; several tokens seldom share one while there are
+// fewer pairs than 3/4 of the experts (128 experts of 2048 x 768, top 8: 2
+// tokens 12.8 us against 17.2 by experts, 8 tokens 31.6 against 34.6, 16
+// tokens 53.9 against 53.1). With up to four pairs an expert that together
+// read up to 32 MiB the caches serve them and the launch less counts (7
+// tokens, 10 experts of 1056 x 544, top 3: 9.4 against 11.9 us; 16 tokens,
+// 44 MB, 13.7 against 13.4).
+bool by_pairs(int T, int H, int I, int E, int top_k) {
+  const int64_t pairs = (int64_t)T * top_k;
+  return T == 1 || 4 * pairs <= 3 * (int64_t)E ||
+         (pairs <= 4 * (int64_t)E && pairs * 3 * H * I / 32 * 17 <= (int64_t)32 << 20);
+}
 
-hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const float* weights,
-                      const void* w13, const void* w13_s, const void* w2, const void* w2_s, int T,
-                      int H, int I, int E, int top_k, bool out_fp32, void* y, void* workspace,
-                      hipStream_t stream) {
-  const auto* xb = static_cast<const uint8_t*>(x);
-  const auto* c13 = static_cast<const uint8_t*>(w13);
-  const auto* s13 = static_cast<const uint8_t*>(w13_s);
-  const auto* c2 = static_cast<const uint8_t*>(w2);
-  const auto* s2 = static_cast<const uint8_t*>(w2_s);
-  const int pairs = T * top_k, HB = H / 32, IB = I / 32;
-  // Workspace: the activations, then, with several tokens, the pairs' parts of y.
-  auto* act = static_cast<float*>(workspace);
-  auto* part = act + (int64_t)pairs * I;
-  hipError_t e;
-  if (T == 1) {
-    hipLaunchKernelGGL(moe_one_up_kernel, dim3(I / 2, top_k),
-                       dim3(64 * even_waves((HB + 63) / 64, kMaxWaves)), 0, stream, xb, ids, c13,
-                       s13, HB, I, E, act);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 threads(64 * even_waves((top_k * IB + 63) / 64, kOneDownWaves));
-    hipLaunchKernelGGL(out_fp32 ? moe_one_down_kernel<true> : moe_one_down_kernel<false>,
-                       dim3(H / kOneDownRows), threads, threads.x / 64 * LaneBlocks<8>::kBytes, stream, act, ids, weights, c2, s2, H, IB, E, top_k,
-                       y);
-    return hipGetLastError();
-  }
+// What a call of moe works on.
+struct MoeArgs {
+  const uint8_t* x;
+  int64_t ldx;
+  const int32_t* ids;
+  const float* weights;
+  const uint8_t *w13, *w13_s, *w2, *w2_s;
+  int T, H, I, E, top_k;
+  bool out_fp32;
+  void* y;
+  float* workspace;
+};
+
+hipError_t launch_pairs(const MoeArgs& m, hipStream_t stream) {
+  const int HB = m.H / 32, IB = m.I / 32;
+  hipLaunchKernelGGL(moe_pair_up_kernel, dim3(m.I / 2, m.T * m.top_k),
+                     dim3(64 * even_waves((HB + 63) / 64, kMaxWaves)), 0, stream, m.x, m.ldx, m.ids,
+                     m.w13, m.w13_s, HB, m.I, m.E, m.top_k, m.workspace);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int waves = even_waves((m.top_k * IB + 63) / 64, kPairDownWaves);
+  hipLaunchKernelGGL(m.out_fp32 ? moe_pair_down_kernel<true> : moe_pair_down_kernel<false>,
+                     dim3(m.H / kPairDownRows, m.T), dim3(64 * waves),
+                     waves * LaneBlocks<8>::kBytes, stream, m.workspace, m.ids, m.weights, m.w2,
+                     m.w2_s, m.H, IB, m.E, m.top_k, m.y);
+  return hipGetLastError();
+}
+
+hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
+  const int pairs = m.T * m.top_k, HB = m.H / 32, IB = m.I / 32, E = m.E;
+  // Workspace: the activations, then the pairs' parts of y.
+  float* act = m.workspace;
+  float* part = act + (int64_t)pairs * m.I;
   const int chosen = pairs < E ? pairs : E;
-  const UpArgs up = {xb, ldx, c13, s13, act, HB, I, top_k};
-  const int64_t up_tiles = I / kFewTile, up_units = (HB + kUnitBlocks - 1) / kUnitBlocks;
+  const UpArgs up = {m.x, m.ldx, m.w13, m.w13_s, act, HB, m.I, m.top_k};
+  const int64_t up_tiles = m.I / kFewTile, up_units = (HB + kUnitBlocks - 1) / kUnitBlocks;
   const bool up_waves = up_tiles * chosen >= kManyTiles;
   const auto launch_up = [&](auto kernel, int lds) {
-    return launch_tiles(kernel, lds, up, up_tiles, up_units, up_waves, ids, pairs, E, stream);
+    return launch_tiles(kernel, lds, up, up_tiles, up_units, up_waves, m.ids, pairs, E, stream);
   };
+  hipError_t e;
   if (pairs > 6 * E)
     e = launch_up(up_waves ? moe_up_kernel<4, true> : moe_up_kernel<4, false>,
                   few_lds_bytes<2, BfRows<4>>());
@@ -500,14 +526,15 @@ hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const floa
     e = launch_up(up_waves ? moe_up_kernel<2, true> : moe_up_kernel<2, false>,
                   few_lds_bytes<2, BfRows<2>>());
   if (e != hipSuccess) return e;
-  const DownArgs down = {act, c2, s2, part, H, I};
-  const int64_t down_tiles = H / (2 * kFewTile), down_units = (IB + kUnitBlocks - 1) / kUnitBlocks;
+  const DownArgs down = {act, m.w2, m.w2_s, part, m.H, m.I};
+  const int64_t down_tiles = m.H / (2 * kFewTile);
+  const int64_t down_units = (IB + kUnitBlocks - 1) / kUnitBlocks;
   const bool down_waves = down_tiles * chosen >= kManyTiles;
   const auto launch_down = [&](auto kernel, int lds) {
-    return launch_tiles(kernel, lds, down, down_tiles, down_units, down_waves, ids, pairs, E,
-                        stream);
+    return launch_tiles(kernel, lds, down, down_tiles, down_units, down_waves, m.ids, pairs,
+                        E, stream);
   };
-  if (out_fp32)
+  if (m.out_fp32)
     e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>,
                     few_lds_bytes<2, F32Rows<4, 3>>());
   else if (pairs > 4 * E)
@@ -517,10 +544,24 @@ hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const floa
     e = launch_down(down_waves ? moe_down_kernel<4, 2, true> : moe_down_kernel<4, 2, false>,
                     few_lds_bytes<2, F32Rows<4, 2>>());
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(out_fp32 ? moe_sum_kernel<true> : moe_sum_kernel<false>,
-                     dim3((H / 2 + kSumThreads - 1) / kSumThreads, T), dim3(kSumThreads), 0, stream, part, ids, weights, H, E,
-                     top_k, y);
+  hipLaunchKernelGGL(m.out_fp32 ? moe_sum_kernel<true> : moe_sum_kernel<false>,
+                     dim3((m.H / 2 + kSumThreads - 1) / kSumThreads, m.T), dim3(kSumThreads), 0,
+                     stream, part, m.ids, m.weights, m.H, E, m.top_k, m.y);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe(const void* x, int64_t ldx, const int32_t* ids, const float* weights,
+                      const void* w13, const void* w13_s, const void* w2, const void* w2_s, int T,
+                      int H, int I, int E, int top_k, bool out_fp32, void* y, void* workspace,
+                      hipStream_t stream) {
+  const MoeArgs m = {static_cast<const uint8_t*>(x),    ldx,
+                     ids,                               weights,
+                     static_cast<const uint8_t*>(w13),  static_cast<const uint8_t*>(w13_s),
+                     static_cast<const uint8_t*>(w2),   static_cast<const uint8_t*>(w2_s),
+                     T, H, I, E, top_k, out_fp32, y, static_cast<float*>(workspace)};
+  return by_pairs(T, H, I, E, top_k) ? launch_pairs(m, stream) : launch_experts(m, stream);
 }
 
 }  // namespace mxfp4

@@ -273,6 +273,10 @@ def run_moe(x, ids, w, ex, **kw):
     # experts, and tiles that fill no workgroup.
     (128, 1024, 512, 64, 8, 0.1), (16, 288, 288, 1000, 16, 0.2), (2, 160, 1056, 9, 9, 0.3),
     (1, 96, 224, 40, 32, 0.5),
+    # By experts: fewer pairs than experts (K split over waves, and a tile a
+    # wave), and few experts of many pairs each.
+    (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (40, 160, 288, 3, 2, 0.1),
+    (64, 128, 96, 16, 8, 0.0), (100, 32, 32, 2, 1, 0.5),
 ])
 def test_moe_matches_the_oracle(T, H, I, E, k, absent, out):
     announce(f"moe T{T} H{H} I{I} E{E} k{k} absent {absent} {out}")
@@ -284,12 +288,13 @@ def test_moe_matches_the_oracle(T, H, I, E, k, absent, out):
     check(got, *fewtoken.moe(x, ids, w, *ex))
 
 
-def test_moe_absent_repeated_and_out_of_range_experts():
+@pytest.mark.parametrize("T", [4, 20])
+def test_moe_absent_repeated_and_out_of_range_experts(T):
     """Tokens with no expert here give zeros (NaN weights beside them are
     not read into the sum), every pair may name the same expert, an expert
     may be named twice by a token, and ids far outside count as absent."""
-    announce("moe unusual choices")
-    T, H, I, E, k = 20, 96, 160, 5, 4
+    announce(f"moe unusual choices, {T} tokens")
+    H, I, E, k = 96, 160, 5, 4
     x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 1)
     ex = experts(E, H, I, 3)
     ids, w = choices(T, E, k, 2)
@@ -307,9 +312,10 @@ def test_moe_absent_repeated_and_out_of_range_experts():
     check(run_moe(x, one, w[3:4].repeat(T, 0), ex), *fewtoken.moe(x, one, w[3:4].repeat(T, 0), *ex))
 
 
-def test_moe_non_finite_tokens_stay_alone():
-    announce("moe NaN and overflowing tokens")
-    T, H, I, E, k = 8, 64, 96, 4, 2
+@pytest.mark.parametrize("T", [8, 24])
+def test_moe_non_finite_tokens_stay_alone(T):
+    announce(f"moe NaN and overflowing tokens among {T}")
+    H, I, E, k = 64, 96, 4, 2
     x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 1)
     ex = experts(E, H, I, 5)
     ids, w = choices(T, E, k, 6)
@@ -318,16 +324,17 @@ def test_moe_non_finite_tokens_stay_alone():
     bad[3, 10] = 0x7FC0                        # NaN
     bad[5, :] = 0x7F00                         # 2^127: the activation overflows
     got = run_moe(bad, ids, w, ex, out_dtype=torch.float32)
-    rows = [0, 1, 2, 4, 6, 7]
+    rows = [t for t in range(T) if t not in (3, 5)]
     check(got[rows], want[rows], tol[rows])
     assert torch.isnan(got[3]).all() and not torch.isfinite(got[5]).any()
 
 
-def test_moe_strides_canaries_and_bits():
+@pytest.mark.parametrize("T", [5, 11])
+def test_moe_strides_canaries_and_bits(T):
     """x rows strided among NaN, unaligned scales, canaries around y and the
     workspace, and the same bits from every run."""
-    announce("moe strides and canaries")
-    T, H, I, E, k = 11, 160, 96, 7, 3
+    announce(f"moe strides and canaries, {T} tokens")
+    H, I, E, k = 160, 96, 7, 3
     x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 1)
     c1, s1, c2, s2 = experts(E, H, I, 7)
     ids, w = choices(T, E, k, 8, 0.2)
@@ -350,11 +357,11 @@ def test_moe_strides_canaries_and_bits():
             assert torch.equal(mx.moe(*args, out_dtype=dt), out)
 
 
-@pytest.mark.parametrize("T,k", [(1, 6), (3, 4), (64, 6)])
-def test_moe_workspace_may_hold_anything(T, k):
+@pytest.mark.parametrize("T,k,E", [(1, 6, 48), (3, 4, 48), (64, 6, 48), (64, 6, 8)])
+def test_moe_workspace_may_hold_anything(T, k, E):
     """A workspace of NaN, and absent experts whose part of it nothing writes."""
-    announce(f"moe with a workspace of NaN, {T} tokens")
-    H, I, E = 512, 288, 48
+    announce(f"moe with a workspace of NaN, {T} tokens, {E} experts")
+    H, I = 512, 288
     x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 1)
     ids, w = choices(T, E, k, 2, 0.4)
     ex = experts(E, H, I, 3)

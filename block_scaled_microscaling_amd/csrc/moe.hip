@@ -5,12 +5,14 @@
 //   a[p, i] = silu(sum_h Wg_e[i, h] x[t, h]) * (sum_h Wu_e[i, h] x[t, h])
 //   y[t, h] = sum_j weights[t, j] sum_i W2_e[h, i] a[p, i]
 // Weights are exact in BF16, sums and a are FP32. The second product takes a
-// as FP32 (one token) or as the sum of BF16 pieces in columns of the same
+// as FP32 (by pairs) or as the sum of BF16 pieces in columns of the same
 // MFMA: three, all of FP32's significand, for FP32 results; two, 16 bits, for
 // BF16 results, whose own rounding is 2^8 times larger.
 //
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
-// once: HBM.
+// once: HBM (1 token through 2 of 8 experts of 4096 x 14336, 187 MB, 22 + 16
+// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 41 + 26 + 5 us), or
+// latency where they are few (1 token through 8 of the latter, 5.2 + 4.7 us).
 //
 // Few pairs: as gemv's one-row kernel, in two launches. The first kernel's
 // workgroup has two gate and two up rows of a pair's expert; the second's
@@ -194,7 +196,7 @@ __device__ __forceinline__ int expert_pairs(const int32_t* __restrict__ ids, int
 
 // Products of two tiles of 16 weight rows, at the uniform rows row0 and row1,
 // with X's columns, K split over the workgroup's waves; the results are left
-// in LDS: part w of (tile t, row r, column c) at tile_at(t, r, c) + 256 w.
+// in LDS, for tile_sum.
 template <class X>
 __device__ __forceinline__ void two_tiles(const uint8_t* codes, const uint8_t* scales,
                                           int64_t row0, int64_t row1, int KB, const X& rows,
@@ -217,6 +219,7 @@ __device__ __forceinline__ void two_tiles(const uint8_t* codes, const uint8_t* s
   __syncthreads();
 }
 
+// Row r and column c of tile t of two_tiles' products.
 __device__ __forceinline__ float tile_sum(const uint8_t* lds, int t, int r, int c) {
   const int waves = blockDim.x >> 6;
   const float* p = reinterpret_cast<const float*>(lds) + t * waves * 256 + (r & 3) * 64 +
@@ -361,8 +364,8 @@ __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0
   const uint8_t* wc[2] = {g.w2 + row * IB * 16, g.w2 + (row + kFewTile) * IB * 16};
   const uint8_t* ws[2] = {g.w2_s + row * IB, g.w2_s + (row + kFewTile) * IB};
   v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, down_rows<X>(g, list, p0, n), IB, 0, 1, lds,
-                acc);
+  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, down_rows<X>(g, list, p0, n), IB, 0,
+                      1, lds, acc);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     // The sum of the pieces' columns.
@@ -453,8 +456,8 @@ constexpr int64_t kManyTiles = 2048;
 
 // `tiles` tiles of each expert, of `units` units of K.
 template <class Kernel, class Args>
-hipError_t launch_tiles(Kernel kernel, int lds_per_wave, const Args& g, int64_t tiles, int64_t units,
-                        bool wave_tiles, const int32_t* ids, int pairs, int E,
+hipError_t launch_tiles(Kernel kernel, int lds_per_wave, const Args& g, int64_t tiles,
+                        int64_t units, bool wave_tiles, const int32_t* ids, int pairs, int E,
                         hipStream_t stream) {
   const int waves = wave_tiles ? kTileWaves : even_waves((int)units, kTileWaves);
   const dim3 grid(wave_tiles ? (tiles + kTileWaves - 1) / kTileWaves : tiles,
@@ -518,8 +521,14 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   const auto launch_up = [&](auto kernel, int lds) {
     return launch_tiles(kernel, lds, up, up_tiles, up_units, up_waves, m.ids, pairs, E, stream);
   };
+  // Columns for up to 16 pairs in the first kernel, 8 in the second, cost
+  // registers, and waves, where most experts have few: from 4 and 2 pairs an
+  // expert on they pay (64 experts of 1024 x 1024, top 8, pairs an expert 2:
+  // 27.1 us with 8 and 8, 28.0 with 16 and 8, 29.3 with 8 and 4; 4: 35.5, 34.7
+  // and 37.8; 16: 70.3, 64.6 and 79.2; 64 experts of 4096 x 1024, 1.6: 83.1,
+  // 88.0 and 82.5).
   hipError_t e;
-  if (pairs > 6 * E)
+  if (pairs >= 4 * E)
     e = launch_up(up_waves ? moe_up_kernel<4, true> : moe_up_kernel<4, false>,
                   few_lds_bytes<2, BfRows<4>>());
   else
@@ -537,7 +546,7 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   if (m.out_fp32)
     e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>,
                     few_lds_bytes<2, F32Rows<4, 3>>());
-  else if (pairs > 4 * E)
+  else if (pairs >= 2 * E)
     e = launch_down(down_waves ? moe_down_kernel<8, 2, true> : moe_down_kernel<8, 2, false>,
                     few_lds_bytes<2, F32Rows<8, 2>>());
   else

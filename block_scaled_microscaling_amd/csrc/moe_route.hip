@@ -5,10 +5,10 @@
 // bits, and 64-bit sums make that independent of the summation order for
 // all practical inputs), p = exp(l - max l) / sum exp(l - max l) in FP32.
 //
-// What bounds it: launches and the latency of two loads in a row; the sums
-// are 2 T E H flop of 64-bit arithmetic (33 MFMA-cycles a KiB of router),
-// the router's and x's bytes are few and come from L2 for all but the first
-// tokens.
+// What bounds it: a few tokens' launches and latencies (1 token x 4096, 8
+// experts 3.9 us; 64 tokens x 4096, 128 experts 5.0 + 4.0), many tokens' 2 T E
+// H flop of 64-bit arithmetic (512 tokens x 4096, 128 experts 20 us). The
+// bytes are few.
 //
 // Few experts: one workgroup a token does it all (one launch). Otherwise the
 // logits are tiles of v_mfma_f64_16x16x4_f64 whose K is split over
@@ -28,7 +28,7 @@ constexpr int kOneExperts = 4;       // that a wave takes at once
 constexpr int kOneMaxExperts = 256;  // LDS: 16 partial sums of each
 constexpr int kTile = 16;            // tokens and experts of an MFMA
 constexpr int kTileWaves = 8;
-constexpr int kSplits = 8;
+constexpr int kMaxSplits = 8;
 
 __device__ __forceinline__ double lo_bf16(uint32_t w) { return (double)__uint_as_float(w << 16); }
 __device__ __forceinline__ double hi_bf16(uint32_t w) {
@@ -281,16 +281,24 @@ hipError_t launch_top(const double* logits, int T, int E, int top_k, int renorma
   return hipGetLastError();
 }
 
+// One workgroup a token does all of 64-bit arithmetic on one CU: up to 64 Ki
+// products and a token a CU that is no slower than the tiles (16 tokens x
+// 4096, 8 and 16 experts 6.4 and 7.4 us against 7.2 and 7.6; 32 experts 9.1
+// against 7.7; 512 tokens x 1024, 32 experts 8.9 against 7.6) and saves the
+// host a launch.
 bool one_launch(int64_t T, int64_t H, int64_t E) {
-  // One workgroup a token takes E H / 64 wave instructions of 64-bit
-  // arithmetic on one CU; tokens beyond the CUs' number wait.
-  return E <= kOneMaxExperts && E * H <= 65536 && T <= 512;
+  return E <= kOneMaxExperts && E * H <= 65536 && T <= 256;
 }
 
+// K's split over workgroups: the tiles are bound by 64-bit arithmetic, so up
+// to a workgroup a CU (H = 4096: 32 tiles 18.8 us whole, 8.3 in 8 parts; 120
+// tiles 18.9 whole, 12.9 in 2, 12.8 in 8; H = 1024: 32 tiles 9.5 and 7.4, 120
+// tiles 9.6 whole, 8.2 in 2, 10.8 in 8).
 int splits_of(int64_t T, int64_t E) {
-  // Fewer tiles than half the CUs: K is split over workgroups.
   const int64_t tiles = ((T + kTile - 1) / kTile) * ((E + kTile - 1) / kTile);
-  return tiles < 128 ? kSplits : 1;
+  int splits = 1;
+  while (splits < kMaxSplits && 2 * splits * tiles <= 256) splits *= 2;
+  return splits;
 }
 
 }  // namespace
@@ -317,9 +325,11 @@ hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int 
                      dim3(64 * kTileWaves), 0, stream, xb, ldx, rb, T, H, E, logits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return splits == 1
-             ? launch_top<1>(logits, T, E, top_k, renorm, ids, weights, stream)
-             : launch_top<kSplits>(logits, T, E, top_k, renorm, ids, weights, stream);
+  const auto top = splits == 1   ? launch_top<1>
+                   : splits == 2 ? launch_top<2>
+                   : splits == 4 ? launch_top<4>
+                                 : launch_top<8>;
+  return top(logits, T, E, top_k, renorm, ids, weights, stream);
 }
 
 }  // namespace mxfp4

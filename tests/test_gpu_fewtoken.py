@@ -35,10 +35,11 @@ def check(got, want, tol, what=""):
 
 
 # ------------------------------------------------------------------- gemv
-def test_gemv_decodes_every_code_and_scale_exactly():
+@pytest.mark.parametrize("M", [1, 2])
+def test_gemv_decodes_every_code_and_scale_exactly(M):
     """One column of ones picks each weight: codes 0..15 in each place of a
     block under scale bytes 0..252, each result the exact value."""
-    announce("gemv decode of every code under every scale")
+    announce(f"gemv decode of every code under every scale, {M} rows")
     K, N = 32, 16 * 253
     codes = np.zeros((N, 16), np.uint8)
     scales = np.repeat(np.arange(253, dtype=np.uint8), 16)[:, None]
@@ -46,12 +47,12 @@ def test_gemv_decodes_every_code_and_scale_exactly():
         codes[:] = 0
         code = np.tile(np.arange(16, dtype=np.uint8), 253)
         codes[:, place // 2] = code << (4 * (place % 2))
-        x = np.zeros((1, K), np.uint16)
-        x[0, place] = 0x3F80                    # 1.0
+        x = np.zeros((M, K), np.uint16)
+        x[M - 1, place] = 0x3F80                # 1.0
         y = mx.gemv(bf16_to_dev(x), u8_to_dev(codes), u8_to_dev(scales),
                     out_dtype=torch.float32)
         want = oracle.dequantize(codes, scales)[:, place]
-        got = host(y)[0]
+        got = host(y)[M - 1]
         normal = np.abs(want) >= 2.0 ** -126
         assert np.array_equal(got[normal], want[normal]), place
         # Below the normal range: the value or zero.
@@ -140,6 +141,17 @@ def test_gemv_non_finite_inputs_stay_in_their_row():
     check(got[rows][:, cols], want[np.ix_(rows, cols)], tol[np.ix_(rows, cols)])
     assert torch.isnan(got[1]).all() and torch.isnan(got[:, 7]).all()
     assert not torch.isfinite(got[4, cols]).any()
+
+
+@pytest.mark.parametrize("M", [1, 6, 30])
+def test_gemv_gives_the_same_bits_every_time(M):
+    announce(f"gemv repeated, {M} rows")
+    N, K = 2000, 4128
+    x = bf16_to_dev(bf16_matrix((M, K), N01, 1))
+    w = u8_to_dev(random_codes(N, K, 2)), u8_to_dev(random_scales(N, K, 3))
+    first = mx.gemv(x, *w, out_dtype=torch.float32)
+    for _ in range(5):
+        assert torch.equal(mx.gemv(x, *w, out_dtype=torch.float32), first)
 
 
 def test_gemv_past_2_32_bytes():
@@ -275,7 +287,7 @@ def run_moe(x, ids, w, ex, **kw):
     (1, 96, 224, 40, 32, 0.5),
     # By experts: fewer pairs than experts (K split over waves, and a tile a
     # wave), and few experts of many pairs each.
-    (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (40, 160, 288, 3, 2, 0.1),
+    (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (20, 1024, 1152, 20, 3, 0.1), (40, 160, 288, 3, 2, 0.1),
     (64, 128, 96, 16, 8, 0.0), (100, 32, 32, 2, 1, 0.5),
 ])
 def test_moe_matches_the_oracle(T, H, I, E, k, absent, out):

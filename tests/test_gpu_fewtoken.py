@@ -68,6 +68,8 @@ def test_gemv_decodes_every_code_and_scale_exactly(M):
     # Enough tiles for two a workgroup; one row over many rounds of K.
     (3, 5000, 352), (5, 6177, 736), (16, 6200, 544), (40, 4001, 96), (2, 24, 32), (1, 9, 33024),
     (6, 40, 33024),
+    # Enough workgroups for their waves to share x: one unit of K, odd ones.
+    (6, 14400, 256), (5, 14341, 800), (16, 14337, 4128), (50, 3600, 288), (9, 20000, 544),
 ])
 def test_gemv_matches_the_oracle(M, N, K, out):
     announce(f"gemv {M}x{N}x{K} {out}")
@@ -143,10 +145,53 @@ def test_gemv_non_finite_inputs_stay_in_their_row():
     assert not torch.isfinite(got[4, cols]).any()
 
 
-@pytest.mark.parametrize("M", [1, 6, 30])
-def test_gemv_gives_the_same_bits_every_time(M):
-    announce(f"gemv repeated, {M} rows")
-    N, K = 2000, 4128
+def test_gemv_of_shared_rows_strided_and_not_finite():
+    """Many weight rows, so that waves share x: rows of a larger buffer of NaN,
+    two rows and one weight row not finite, nothing around y written."""
+    announce("gemv with shared x, strided, NaN and Inf")
+    M, N, K = 19, 6001, 864
+    x = bf16_matrix((M, K), N01, 1)
+    codes, scales = random_codes(N, K, 2), random_scales(N, K, 3)
+    want, tol = fewtoken.gemv(x, codes, scales)
+    bad = x.copy()
+    bad[1, 863] = 0x7FC0                       # NaN in the last block
+    bad[18, 3] = 0x7F80                        # Inf
+    scales_nan = scales.copy()
+    scales_nan[6000, 26] = 255                 # the last weight row's last scale
+    big = torch.full((2 * M, K + 24), float("nan"), dtype=torch.bfloat16, device=DEV)
+    xs = big[::2, 8:8 + K]
+    xs.copy_(bf16_to_dev(bad))
+    buf = torch.full((M * N + 64,), 7.0, device=DEV)
+    out = buf[32:32 + M * N].view(M, N)
+    got = mx.gemv(xs, u8_to_dev(codes), u8_to_dev(scales_nan), out=out)
+    rows = [m for m in range(M) if m not in (1, 18)]
+    check(got[rows][:, :N - 1], want[rows][:, :N - 1], tol[rows][:, :N - 1])
+    assert torch.isnan(got[1]).all() and torch.isnan(got[:, N - 1]).all()
+    assert not torch.isfinite(got[18]).any()
+    assert torch.all(buf[:32] == 7.0) and torch.all(buf[32 + M * N:] == 7.0)
+
+
+@pytest.mark.parametrize("M,N", [(8, 300), (16, 700), (9, 10241)])
+def test_gemv_decodes_codes_and_scales_in_every_kernel(M, N):
+    """x of ones in one block each: each result is a sum of 32 exact values."""
+    announce(f"gemv of ones, {M} rows x {N}")
+    K = 32 * 24
+    codes, scales = random_codes(N, K, N), random_scales(N, K, M)
+    x = np.zeros((M, K), np.uint16)
+    for m in range(M):
+        b = (m * 5 + 3) % 24
+        x[m, 32 * b:32 * b + 32] = 0x3F80      # 1.0
+    got = mx.gemv(bf16_to_dev(x), u8_to_dev(codes), u8_to_dev(scales), out_dtype=torch.float32)
+    want = oracle.dequantize(codes, scales).reshape(N, 24, 32).sum(2)
+    want = np.stack([want[:, (m * 5 + 3) % 24] for m in range(M)])
+    # 32 values of at most 12 half-steps of one scale add exactly.
+    assert np.array_equal(host(got), want)
+
+
+@pytest.mark.parametrize("M,N", [(1, 2000), (6, 2000), (30, 2000), (30, 6000)])
+def test_gemv_gives_the_same_bits_every_time(M, N):
+    announce(f"gemv repeated, {M} rows x {N}")
+    K = 4128
     x = bf16_to_dev(bf16_matrix((M, K), N01, 1))
     w = u8_to_dev(random_codes(N, K, 2)), u8_to_dev(random_scales(N, K, 3))
     first = mx.gemv(x, *w, out_dtype=torch.float32)

@@ -145,22 +145,22 @@ constexpr int kUnitBlocks = 8;
 constexpr int kXStride = 256 + 16;  // LDS row strides: padded, so that the
 constexpr int kWStride = 128 + 16;  // fragment reads meet no bank conflicts
 
-// Activations for few_stream: 4 XL BF16 rows, one a column. Lane l loads rows
-// 4 i + l / 16, 16 bytes each.
-template <int XL>
+// Activations for few_stream: 4 XL BF16 rows, one a column, whose blocks start
+// kBlockBytes apart. Lane l loads rows 4 i + l / 16, 16 bytes each.
+template <int XL, int kBlockBytes = 64>
 struct BfRows {
   static constexpr int kColumns = 4 * XL;
   struct Half {
     u32x4_t r[XL];
   };
-  const uint8_t* p[XL];  // the lane's rows, plus its place in a block (l % 4) * 16
+  const uint8_t* p[XL];  // the lane's rows, with its place (l % 4) in a block
 
   // Half h (128 k) of unit u; blocks past the row are read as its last.
   __device__ __forceinline__ void load(Half& a, int u, int h, int KB) const {
     const int b = min(u * kUnitBlocks + h * 4 + (int)((threadIdx.x & 15) >> 2), KB - 1);
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      a.r[i] = *reinterpret_cast<const u32x4_t*>(p[i] + (int64_t)b * 64);
+      a.r[i] = *reinterpret_cast<const u32x4_t*>(p[i] + (int64_t)b * kBlockBytes);
   }
   // Zeros in place of the blocks from nb of the unit.
   __device__ __forceinline__ void cut(Half& a, int h, int nb) const {
@@ -175,54 +175,6 @@ struct BfRows {
     for (int i = 0; i < XL; ++i)
       *reinterpret_cast<u32x4_t*>(lds + (4 * i + (lane >> 4)) * kXStride + (lane & 15) * 16) =
           a.r[i];
-  }
-};
-
-// Activations for few_stream: kRows (even) FP32 rows, each as the sum of
-// kPieces BF16 values in columns piece * kRows + row. Every rounding leaves a
-// rest that FP32 holds exactly, at most 2^-9 of the value, so two pieces give
-// 16 bits of significand and three all 24 (values below 2^-100 fewer). Lane l
-// loads rows 2 i + l / 32, 4 values each.
-template <int kRowCount, int kPieces>
-struct F32Rows {
-  static constexpr int kRows = kRowCount;
-  static constexpr int kColumns = kRows * kPieces;
-  struct Half {
-    v4f_t r[kRows / 2];
-  };
-  const float* p[kRows / 2];  // the lane's rows, plus its place in a block (l % 8) * 4
-
-  __device__ __forceinline__ void load(Half& a, int u, int h, int KB) const {
-    const int b = min(u * kUnitBlocks + h * 4 + (int)((threadIdx.x & 31) >> 3), KB - 1);
-#pragma unroll
-    for (int i = 0; i < kRows / 2; ++i)
-      a.r[i] = *reinterpret_cast<const v4f_t*>(p[i] + (int64_t)b * 32);
-  }
-  __device__ __forceinline__ void cut(Half& a, int h, int nb) const {
-    if (h * 4 + (int)((threadIdx.x & 31) >> 3) >= nb) {
-#pragma unroll
-      for (int i = 0; i < kRows / 2; ++i) a.r[i] = v4f_t{};
-    }
-  }
-  __device__ __forceinline__ void park(const Half& a, uint8_t* lds) const {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < kRows / 2; ++i) {
-      float v[4] = {a.r[i][0], a.r[i][1], a.r[i][2], a.r[i][3]};
-#pragma unroll
-      for (int piece = 0; piece < kPieces; ++piece) {
-        const uint32_t w0 = pack_bf16x2(v[0], v[1]), w1 = pack_bf16x2(v[2], v[3]);
-        *reinterpret_cast<uint2*>(lds + (piece * kRows + 2 * i + (lane >> 5)) * kXStride +
-                                  (lane & 31) * 8) = make_uint2(w0, w1);
-        if (piece + 1 < kPieces) {
-          // No rest where the piece is no finite number: inf - inf is NaN.
-          const uint32_t bits[4] = {w0 << 16, w0 & 0xFFFF0000u, w1 << 16, w1 & 0xFFFF0000u};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = (bits[j] & 0x7F800000u) == 0x7F800000u ? 0.0f : v[j] - __uint_as_float(bits[j]);
-        }
-      }
-    }
   }
 };
 
@@ -330,6 +282,140 @@ __device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
       }
     }
     wave_sync();
+  }
+}
+
+// The next BF16 piece of v, which becomes its rest: FP32 holds it exactly, at
+// most 2^-9 of the value.
+__device__ __forceinline__ uint16_t next_piece(float& v) {
+  const uint32_t bits = pack_bf16x2(v, v) << 16;
+  // No rest where the piece is no finite number: inf - inf is NaN.
+  v = (bits & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(bits);
+  return (uint16_t)(bits >> 16);
+}
+
+// Products for workgroups whose waves share x: waves are kShareTiles tiles of
+// 16 weight rows times `parts` parts of K. The four waves of a part load a
+// quarter each of a unit of its 4 XL rows of x into LDS. Up to 16 rows are
+// double-buffered, with one barrier a unit; for 32 that LDS would cost waves.
+constexpr int kShareTiles = 4;
+constexpr int kShareStride = 512 + 16;  // LDS row stride of a unit of x, padded
+
+// An LDS barrier of the workgroup that leaves global loads in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <int XL>
+constexpr int share_x_bytes() {  // of one part of K
+  return (XL > 4 ? 1 : 2) * 4 * XL * kShareStride;
+}
+
+template <int XL>
+constexpr int share_lds_bytes(int parts) {
+  return parts * (share_x_bytes<XL>() + kShareTiles * kFewTile * kWStride);
+}
+
+// Adds to acc the products of weight rows row(0 .. 15), counted from codes and
+// scales (KB blocks a row, within 2^32 bytes), with the rows of x at xrow(0 ..
+// 4 XL - 1), given with the lane's place (lane % 4) in a block and blocks that
+// start kBlockBytes apart, over the units part, part + parts, ...; tile is the
+// wave's in its part. Column c of x's rows is column c % 16 of acc[c / 16].
+template <int XL, int kBlockBytes, class Row, class XRow>
+__device__ __forceinline__ void share_stream(const uint8_t* codes, const uint8_t* scales,
+                                             const Row& row, const XRow& xrow, int KB, int tile,
+                                             int part, int parts, uint8_t* lds,
+                                             v4f_t (&acc)[(XL + 3) / 4]) {
+  // Pieces of a unit of x: 4 rows x 256 bytes, one load of a wave each.
+  constexpr int kColumns = 4 * XL, kPieces = 2 * XL, kGroups = (XL + 3) / 4;
+  constexpr int kMine = (kPieces + kShareTiles - 1) / kShareTiles;
+  constexpr bool kTwoBuffers = XL <= 4;
+  constexpr int kBuffer = kTwoBuffers ? kColumns * kShareStride : 0;
+  const int lane = threadIdx.x & 63;
+  const int a = lane & 15, g = lane >> 4, blk = lane & 7;
+  uint8_t* xl = lds + part * share_x_bytes<XL>();
+  uint8_t* wl =
+      lds + parts * share_x_bytes<XL>() + (part * kShareTiles + tile) * kFewTile * kWStride;
+  const int column = min(a, kColumns - 1);
+  const int units = (KB + kUnitBlocks - 1) / kUnitBlocks;
+  uint32_t cp[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) cp[d] = (uint32_t)row(8 * d + (lane >> 3)) * KB * 16;
+  const uint32_t sp = (uint32_t)row(a) * KB;
+  const uint8_t* xp[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    xp[i] = xrow((4 * ((tile + i * kShareTiles) >> 1) + g) % kColumns);
+  u32x4_t w[2], xr[kMine];
+  uint64_t sc, cs = 0;
+  const auto load = [&](int u) {
+    const uint32_t at = (uint32_t)min(u * kUnitBlocks + blk, KB - 1) * 16;
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      w[d] = *reinterpret_cast<const u32x4_t*>(codes + (cp[d] + at));
+    if (KB >= kUnitBlocks) {
+      const uint32_t from = (uint32_t)min(u * kUnitBlocks, KB - kUnitBlocks);
+      __builtin_memcpy(&sc, scales + (sp + from), 8);
+    } else {
+      sc = 0;
+      for (int i = 0; i < KB; ++i)
+        sc |= (uint64_t)scales[sp + i] << (8 * (kUnitBlocks - KB + i));
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int piece = tile + i * kShareTiles;
+      if (piece >= kPieces) break;
+      const int b = min(u * kUnitBlocks + (piece & 1) * 4 + (a >> 2), KB - 1);
+      xr[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (int64_t)b * kBlockBytes);
+    }
+  };
+  const auto park = [&](int u, int buffer) {
+    // Blocks past the row: scale 1 and activations of zero.
+    const int nb = KB - u * kUnitBlocks;
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      *reinterpret_cast<u32x4_t*>(wl + (8 * d + (lane >> 3)) * kWStride + blk * 16) = w[d];
+    cs = sc;
+    if (nb < kUnitBlocks)
+      cs = (cs >> (8 * (kUnitBlocks - nb))) | (0x7F7F7F7F7F7F7F7Full << (8 * nb));
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int piece = tile + i * kShareTiles, half = piece & 1;
+      if (piece >= kPieces) break;
+      if (half * 4 + (a >> 2) >= nb) xr[i] = u32x4_t{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4_t*>(xl + buffer * kBuffer + (4 * (piece >> 1) + g) * kShareStride +
+                                  half * 256 + a * 16) = xr[i];
+    }
+  };
+
+  int u = part;
+  if (u < units) {
+    load(u);
+    park(u, 0);
+  }
+  // Every wave meets every barrier, with or without a unit of its own. A
+  // buffer is written again only after the barrier that follows its use.
+  for (int i = 0; i * parts < units; ++i, u += parts) {
+    if (u + parts < units) load(u + parts);
+    lds_barrier();
+    if (u < units) {
+#pragma unroll
+      for (int b = 0; b < kUnitBlocks; ++b) {
+        const uint32_t ww = *reinterpret_cast<const uint32_t*>(wl + a * kWStride + b * 16 + 4 * g);
+        const bf16x8_t wf = decode8(ww, scale_of_byte((uint32_t)(cs >> (8 * b)) & 0xFF));
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+          const bf16x8_t xf = *reinterpret_cast<const bf16x8_t*>(
+              xl + (i & 1) * kBuffer + (16 * q + column) * kShareStride + b * 64 + g * 16);
+          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf, acc[q], 0, 0, 0);
+        }
+      }
+      wave_sync();
+    }
+    if (!kTwoBuffers) lds_barrier();
+    if (u + parts < units) park(u + parts, (i + 1) & 1);
   }
 }
 

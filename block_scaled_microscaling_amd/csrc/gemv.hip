@@ -167,119 +167,33 @@ hipError_t launch_few(const uint8_t* x, int64_t ldx, const uint8_t* codes, const
 // buffered: one barrier a unit. 16 rows x 28672 x 4096: one part of K
 // 15.6 us, two 14.8, four 18.9; two tiles and four parts 23.5, eight tiles
 // 15.2, four tiles with two units in flight 16.2.
-constexpr int kShareTiles = 4;
 constexpr int kShareParts = 2;
-constexpr int kShareStride = 512 + 16;  // LDS row stride of a unit of x, padded
-
-// An LDS barrier of the workgroup that leaves global loads in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-template <int XL>
-constexpr int share_x_bytes() {  // both buffers of one part of K
-  return 2 * 4 * XL * kShareStride;
-}
 
 template <int XL, bool kOutFp32>
 __global__ __launch_bounds__(64 * kShareTiles * kShareParts) void gemv_share_kernel(
     const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ scales, int M, int N, int KB, void* __restrict__ y) {
-  // Pieces of a unit of x: 4 rows x 256 bytes, one load of a wave each.
-  constexpr int kColumns = 4 * XL, kPieces = 2 * XL;
-  constexpr int kMine = (kPieces + kShareTiles - 1) / kShareTiles;
-  constexpr int kBuffer = kColumns * kShareStride;
+  constexpr int kColumns = 4 * XL;
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int parts = (blockDim.x >> 6) / kShareTiles;
-  const int tile = wave % kShareTiles, part = wave / kShareTiles;
-  const int a = lane & 15, g = lane >> 4, blk = lane & 7;
+  const int tile = wave % kShareTiles;
   const int64_t n0 = block_n() * (kShareTiles * kFewTile);
   if (n0 >= N) return;
   const int m0 = blockIdx.y * kFewTile;
   // Rows past the end re-read the last one; they are not stored.
   const int last = (int)min((int64_t)N - 1 - n0, (int64_t)(kShareTiles * kFewTile - 1));
-  codes += n0 * KB * 16;
-  scales += n0 * KB;
-  uint8_t* xl = lds + part * share_x_bytes<XL>();
-  uint8_t* wl = lds + parts * share_x_bytes<XL>() + wave * kFewTile * kWStride;
-  const int column = min(a, kColumns - 1);
-  const int units = (KB + kUnitBlocks - 1) / kUnitBlocks;
-
-  const uint8_t* xp[kMine];
-#pragma unroll
-  for (int i = 0; i < kMine; ++i)
-    xp[i] = x + (int64_t)min(m0 + 4 * ((tile + i * kShareTiles) >> 1) + g, M - 1) * ldx * 2 +
-            (lane & 3) * 16;
-  u32x4_t w[2], xr[kMine];
-  uint64_t sc, cs = 0;
-  const auto load = [&](int u) {
-    const uint32_t at = (uint32_t)min(u * kUnitBlocks + blk, KB - 1) * 16;
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const uint32_t r = (uint32_t)min(kFewTile * tile + 8 * d + (lane >> 3), last);
-      w[d] = *reinterpret_cast<const u32x4_t*>(codes + (r * KB * 16 + at));
-    }
-    const uint32_t from = (uint32_t)min(u * kUnitBlocks, KB - kUnitBlocks);
-    __builtin_memcpy(&sc, scales + ((uint32_t)min(kFewTile * tile + a, last) * KB + from), 8);
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int piece = tile + i * kShareTiles;
-      if (piece >= kPieces) break;
-      const int b = min(u * kUnitBlocks + (piece & 1) * 4 + (a >> 2), KB - 1);
-      xr[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (int64_t)b * 64);
-    }
-  };
-  const auto park = [&](int u, int buffer) {
-    // Blocks past the row: scale 1 and activations of zero.
-    const int nb = KB - u * kUnitBlocks;
-#pragma unroll
-    for (int d = 0; d < 2; ++d)
-      *reinterpret_cast<u32x4_t*>(wl + (8 * d + (lane >> 3)) * kWStride + blk * 16) = w[d];
-    cs = sc;
-    if (nb < kUnitBlocks)
-      cs = (cs >> (8 * (kUnitBlocks - nb))) | (0x7F7F7F7F7F7F7F7Full << (8 * nb));
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int piece = tile + i * kShareTiles, half = piece & 1;
-      if (piece >= kPieces) break;
-      if (half * 4 + (a >> 2) >= nb) xr[i] = u32x4_t{0u, 0u, 0u, 0u};
-      *reinterpret_cast<u32x4_t*>(xl + buffer * kBuffer + (4 * (piece >> 1) + g) * kShareStride +
-                                  half * 256 + a * 16) = xr[i];
-    }
-  };
-
-  v4f_t acc = {};
-  int u = part;
-  if (u < units) {
-    load(u);
-    park(u, 0);
-  }
-  // Every wave meets every barrier, with or without a unit of its own. A
-  // buffer is written again only after the barrier that follows its use.
-  for (int i = 0; i * parts < units; ++i, u += parts) {
-    if (u + parts < units) load(u + parts);
-    lds_barrier();
-    if (u < units) {
-#pragma unroll
-      for (int b = 0; b < kUnitBlocks; ++b) {
-        const bf16x8_t xf = *reinterpret_cast<const bf16x8_t*>(
-            xl + (i & 1) * kBuffer + column * kShareStride + b * 64 + g * 16);
-        const uint32_t ww = *reinterpret_cast<const uint32_t*>(wl + a * kWStride + b * 16 + 4 * g);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            decode8(ww, scale_of_byte((uint32_t)(cs >> (8 * b)) & 0xFF)), xf, acc, 0, 0, 0);
-      }
-      wave_sync();
-    }
-    if (u + parts < units) park(u + parts, (i + 1) & 1);
-  }
+  v4f_t acc[1] = {v4f_t{}};
+  share_stream<XL, 64>(
+      codes + n0 * KB * 16, scales + n0 * KB,
+      [&](int r) { return min(kFewTile * tile + r, last); },
+      [&](int r) { return x + (int64_t)min(m0 + r, M - 1) * ldx * 2 + (lane & 3) * 16; }, KB, tile,
+      wave / kShareTiles, parts, lds, acc);
   __syncthreads();
   auto* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) red[wave * 256 + v * 64 + lane] = acc[v];
+  for (int v = 0; v < 4; ++v) red[wave * 256 + v * 64 + lane] = acc[0][v];
   __syncthreads();
   for (int i = threadIdx.x; i < kShareTiles * 256; i += blockDim.x) {
     // Row i % 16 of column i / 16 % 16, so a token's rows store together.
@@ -296,9 +210,9 @@ template <int XL>
 hipError_t launch_share(const uint8_t* x, int64_t ldx, const uint8_t* codes, const uint8_t* scales,
                         int M, int N, int KB, bool out_fp32, void* y, hipStream_t stream) {
   const int parts = KB > kUnitBlocks ? kShareParts : 1;
-  const int streamed = parts * (share_x_bytes<XL>() + kShareTiles * kFewTile * kWStride);
+  const int streamed = share_lds_bytes<XL>(parts);
   const int lds = streamed > parts * kShareTiles * 1024 ? streamed : parts * kShareTiles * 1024;
-  static_assert(kShareParts * (share_x_bytes<4>() + kShareTiles * kFewTile * kWStride) <= 65536, "");
+  static_assert(share_lds_bytes<4>(kShareParts) <= 65536, "");
   const int64_t rows = kShareTiles * kFewTile;
   const dim3 grid = grid_n(((int64_t)N + rows - 1) / rows, (M + kFewTile - 1) / kFewTile);
   const auto kernel = out_fp32 ? gemv_share_kernel<XL, true> : gemv_share_kernel<XL, false>;

@@ -7,7 +7,8 @@
 // Weights are exact in BF16, sums and a are FP32. The second product takes a
 // as FP32 (by pairs) or as the sum of BF16 pieces in columns of the same
 // MFMA: three, all of FP32's significand, for FP32 results; two, 16 bits, for
-// BF16 results, whose own rounding is 2^8 times larger.
+// BF16 results, whose own rounding is 2^8 times larger. The first kernel by
+// experts writes the pieces, so that they are made once.
 //
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
 // once: HBM (1 token through 2 of 8 experts of 4096 x 14336, 187 MB, 22 + 16
@@ -18,10 +19,12 @@
 // workgroup has two gate and two up rows of a pair's expert; the second's
 // eight rows of a token's y, over the blocks of all its experts one after the
 // other, so the sum over j needs no other workgroup. Many pairs: an expert's
-// weights are read once for all its pairs, by few_stream, and a third launch
-// sums the pairs' parts of y.
+// weights are read once for all its pairs, by few_stream (W2 by share_stream
+// where an expert has many), and a third launch sums the pairs' parts of y.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "fewtoken.h"
 
@@ -32,7 +35,8 @@ constexpr int kMaxWaves = 8;
 constexpr int kPairDownRows = 8;
 constexpr int kPairDownWaves = 7;  // 63 KiB of LDS
 constexpr int kMaxPairs = 1024;
-constexpr int kTileWaves = 4;  // of the kernels for several tokens
+constexpr int kTileWaves = 4;   // of the kernels for several tokens
+constexpr int kDenseParts = 2;  // parts of K of the kernel for many pairs an expert
 
 template <bool kOutFp32>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
@@ -234,8 +238,8 @@ struct UpArgs {
   int64_t ldx;
   const uint8_t* w13;
   const uint8_t* w13_s;
-  float* act;
-  int HB, I, top_k;
+  uint16_t* act;  // [pairs][I / 16][pieces][16]: BF16 pieces of the activations
+  int HB, I, top_k, pieces;
 };
 
 // The tokens of the pairs list[p0 .. p0 + 4 XL); past the n-th, of the last.
@@ -258,11 +262,18 @@ template <int XL>
 __device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
                                         const uint16_t* list, int p0, int n, uint8_t* lds) {
   two_tiles(g.w13, g.w13_s, gate, gate + g.I, g.HB, up_rows<XL>(g, list, p0, n), lds);
-  for (int i = threadIdx.x; i < 64 * XL; i += blockDim.x) {
-    const int r = i & 15, c = i >> 4;
-    if (p0 + c < n)
-      g.act[(int64_t)list[p0 + c] * g.I + i0 + r] =
-          silu_mul(tile_sum(lds, 0, r, c), tile_sum(lds, 1, r, c));
+  for (int i = threadIdx.x; i < 32 * XL; i += blockDim.x) {
+    const int r = 2 * (i & 7), c = i >> 3;
+    if (p0 + c >= n) continue;
+    float v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      v[j] = silu_mul(tile_sum(lds, 0, r + j, c), tile_sum(lds, 1, r + j, c));
+    uint16_t* at = g.act + ((int64_t)list[p0 + c] * g.I + i0) * g.pieces + r;
+    for (int piece = 0; piece < g.pieces; ++piece, at += kFewTile) {
+      const uint32_t low = next_piece(v[0]);
+      *reinterpret_cast<uint32_t*>(at) = low | (uint32_t)next_piece(v[1]) << 16;
+    }
   }
 }
 
@@ -280,7 +291,18 @@ __device__ __forceinline__ void up_wave(const UpArgs& g, int64_t gate, int i0,
   v4f_t v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = silu_mul(acc[0][i], acc[1][i]);
-  *reinterpret_cast<v4f_t*>(g.act + (int64_t)list[p0 + c] * g.I + i0 + 4 * (lane >> 4)) = v;
+  uint16_t* at = g.act + ((int64_t)list[p0 + c] * g.I + i0) * g.pieces + 4 * (lane >> 4);
+  for (int piece = 0; piece < g.pieces; ++piece, at += kFewTile) {
+    uint16_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f = v[i];
+      b[i] = next_piece(f);
+      v[i] = f;
+    }
+    *reinterpret_cast<uint2*>(at) = make_uint2(b[0] | (uint32_t)b[1] << 16,
+                                               b[2] | (uint32_t)b[3] << 16);
+  }
 }
 
 // A workgroup takes 16 activation columns of an expert, or, with kWaveTiles,
@@ -305,7 +327,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void moe_up_kernel(UpArgs g,
     else
       up_tile<XL>(g, gate, i0, list, p0, n, lds);
   };
-  for (int p0 = 0; p0 < n; p0 += 4 * kMaxXL) {
+  for (int p0 = blockIdx.z * 4 * kMaxXL; p0 < n; p0 += gridDim.z * 4 * kMaxXL) {
     const int left = n - p0;
     if (left <= 4)
       take(std::integral_constant<int, 1>{}, p0);
@@ -317,22 +339,36 @@ __global__ __launch_bounds__(64 * kTileWaves) void moe_up_kernel(UpArgs g,
 }
 
 struct DownArgs {
-  const float* act;
+  const uint16_t* act;
   const uint8_t* w2;
   const uint8_t* w2_s;
   float* part;  // [pairs][H]: W2 a of each pair
   int H, I;
 };
 
-// The activations of the pairs list[p0 .. p0 + kRows); past the n-th, of the
-// last.
-template <class X>
-__device__ __forceinline__ X down_rows(const DownArgs& g, const uint16_t* list, int p0, int n) {
-  const int lane = threadIdx.x & 63;
-  X rows;
+// The lane's place in the first block of a pair's piece.
+template <int kPieces>
+__device__ __forceinline__ const uint8_t* piece_at(const DownArgs& g, int p, int piece) {
+  const int q = threadIdx.x & 3;
+  return reinterpret_cast<const uint8_t*>(
+      g.act + (int64_t)p * g.I * kPieces + ((q >> 1) * kPieces + piece) * kFewTile + (q & 1) * 8);
+}
+
+// The pieces of the pairs list[p0 .. p0 + kRows), a piece of all of them after
+// the other; past the n-th pair, of the last.
+template <int kRows, int kPieces>
+using DownRows = BfRows<kRows * kPieces / 4, 64 * kPieces>;
+
+template <int kRows, int kPieces>
+__device__ __forceinline__ DownRows<kRows, kPieces> down_rows(const DownArgs& g,
+                                                              const uint16_t* list, int p0,
+                                                              int n) {
+  DownRows<kRows, kPieces> rows;
 #pragma unroll
-  for (int i = 0; i < X::kRows / 2; ++i)
-    rows.p[i] = g.act + (int64_t)list[min(p0 + 2 * i + (lane >> 5), n - 1)] * g.I + (lane & 7) * 4;
+  for (int i = 0; i < kRows * kPieces / 4; ++i) {
+    const int c = 4 * i + ((threadIdx.x & 63) >> 4);
+    rows.p[i] = piece_at<kPieces>(g, list[min(p0 + c % kRows, n - 1)], c / kRows);
+  }
   return rows;
 }
 
@@ -342,7 +378,7 @@ template <int kRows, int kPieces>
 __device__ __forceinline__ void down_tile(const DownArgs& g, int64_t row, int h0,
                                           const uint16_t* list, int p0, int n, uint8_t* lds) {
   two_tiles(g.w2, g.w2_s, row, row + kFewTile, g.I / 32,
-            down_rows<F32Rows<kRows, kPieces>>(g, list, p0, n), lds);
+            down_rows<kRows, kPieces>(g, list, p0, n), lds);
   for (int i = threadIdx.x; i < 32 * kRows; i += blockDim.x) {
     const int r = i & 31, c = i >> 5;
     if (p0 + c >= n) continue;
@@ -358,20 +394,19 @@ __device__ __forceinline__ void down_tile(const DownArgs& g, int64_t row, int h0
 template <int kRows, int kPieces>
 __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0,
                                           const uint16_t* list, int p0, int n, uint8_t* lds) {
-  using X = F32Rows<kRows, kPieces>;
   const int lane = threadIdx.x & 63, c = lane & 15;
   const int IB = g.I / 32;
   const uint8_t* wc[2] = {g.w2 + row * IB * 16, g.w2 + (row + kFewTile) * IB * 16};
   const uint8_t* ws[2] = {g.w2_s + row * IB, g.w2_s + (row + kFewTile) * IB};
   v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, down_rows<X>(g, list, p0, n), IB, 0,
-                      1, lds, acc);
+  few_stream<2, true>(wc, ws, [](int, int r) { return r; },
+                      down_rows<kRows, kPieces>(g, list, p0, n), IB, 0, 1, lds, acc);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     // The sum of the pieces' columns.
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float sum = c < X::kColumns ? acc[t][i] : 0.0f;
+      float sum = c < kRows * kPieces ? acc[t][i] : 0.0f;
       sum += __shfl_xor(sum, kRows);
       if (kPieces == 3) sum += __shfl_xor(sum, 2 * kRows);
       acc[t][i] = sum;
@@ -395,7 +430,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void moe_down_kernel(
   const int h0 = (kWaveTiles ? blockIdx.x * kTileWaves + wave : blockIdx.x) * 2 * kFewTile;
   if (n == 0 || h0 >= g.H) return;
   const int64_t row = (int64_t)e * g.H + h0;
-  uint8_t* mine = lds + wave * few_lds_bytes<2, F32Rows<kMaxRows, kPieces>>();
+  uint8_t* mine = lds + wave * few_lds_bytes<2, DownRows<kMaxRows, kPieces>>();
   const auto take = [&](auto r, int p0) {
     constexpr int kRows = decltype(r)::value;
     if constexpr (kWaveTiles)
@@ -403,11 +438,84 @@ __global__ __launch_bounds__(64 * kTileWaves) void moe_down_kernel(
     else
       down_tile<kRows, kPieces>(g, row, h0, list, p0, n, lds);
   };
-  for (int p0 = 0; p0 < n; p0 += kMaxRows) {
+  for (int p0 = blockIdx.z * kMaxRows; p0 < n; p0 += gridDim.z * kMaxRows) {
     if (kMaxRows > 4 && n - p0 <= 4)
       take(std::integral_constant<int, 4>{}, p0);
     else
       take(std::integral_constant<int, kMaxRows>{}, p0);
+  }
+}
+
+// The sums of a wave's tiles over the parts of K, in LDS: red[wave][group]
+// [256] of share_stream's acc.
+template <int kGroups>
+__device__ __forceinline__ void share_put(const v4f_t (&acc)[kGroups], uint8_t* lds) {
+  auto* red = reinterpret_cast<float*>(lds) + (threadIdx.x >> 6) * kGroups * 256 +
+              (threadIdx.x & 63);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kGroups; ++q)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[q * 256 + v * 64] = acc[q][v];
+  __syncthreads();
+}
+
+template <int kGroups>
+__device__ __forceinline__ float share_get(const uint8_t* lds, int tile, int r, int c,
+                                           int parts) {
+  const float* p = reinterpret_cast<const float*>(lds) + (tile * kGroups + c / 16) * 256 +
+                   (r & 3) * 64 + (r >> 2) * 16 + c % 16;
+  float sum = p[0];
+  for (int q = 1; q < parts; ++q) sum += p[q * kShareTiles * kGroups * 256];
+  return sum;
+}
+
+// Many pairs an expert. A workgroup takes 64 outputs of an expert and its waves
+// share the pieces of 16 pairs (10 if three pieces), or of half as many, so a
+// weight is decoded once for two products.
+template <int kPieces>
+__global__ __launch_bounds__(64 * kShareTiles * kDenseParts) void moe_dense_down_kernel(
+    DownArgs g, const int32_t* __restrict__ ids, int pairs, int E) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint16_t list[kMaxPairs];
+  const int e = blockIdx.y;
+  const int n = list_pairs(ids, pairs, e, list);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int parts = (blockDim.x >> 6) / kShareTiles;
+  const int tile = wave % kShareTiles, part = wave / kShareTiles;
+  const int h0 = blockIdx.x * kShareTiles * kFewTile;
+  const int last = min(g.H - h0, kShareTiles * kFewTile) - 1;
+  const int64_t row = (int64_t)e * g.H + h0;
+  const int IB = g.I / 32;
+  const auto take = [&](auto xl, int p0) {
+    constexpr int XL = decltype(xl)::value, kGroups = XL / 4, kRows = 4 * XL / kPieces;
+    v4f_t acc[kGroups] = {};
+    share_stream<XL, 64 * kPieces>(
+        g.w2 + row * IB * 16, g.w2_s + row * IB,
+        [&](int r) { return min(kFewTile * tile + r, last); },
+        [&](int c) {
+          return piece_at<kPieces>(g, list[min(p0 + c % kRows, n - 1)],
+                                   min(c / kRows, kPieces - 1));
+        },
+        IB, tile, part, parts, lds, acc);
+    share_put(acc, lds);
+    for (int i = threadIdx.x; i < 64 * kRows; i += blockDim.x) {
+      const int r = i & 63, c = i >> 6;
+      if (p0 + c >= n || r > last) continue;
+      float sum = 0.0f;
+#pragma unroll
+      for (int piece = kPieces - 1; piece >= 0; --piece)
+        sum += share_get<kGroups>(lds, r >> 4, r & 15, piece * kRows + c, parts);
+      g.part[(int64_t)list[p0 + c] * g.H + h0 + r] = sum;
+    }
+    __syncthreads();
+  };
+  constexpr int kMost = 32 / kPieces, kHalf = 16 / kPieces;
+  for (int p0 = blockIdx.z * kMost; p0 < n; p0 += gridDim.z * kMost) {
+    if (n - p0 <= kHalf)
+      take(std::integral_constant<int, 4>{}, p0);
+    else
+      take(std::integral_constant<int, 8>{}, p0);
   }
 }
 
@@ -454,14 +562,28 @@ __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(const float* __res
 // 10 experts of 1056 x 544 (340 tiles): 6.9 + 6.6 us against 5.3 + 5.3.
 constexpr int64_t kManyTiles = 2048;
 
-// `tiles` tiles of each expert, of `units` units of K.
+// Rounds of `most` pairs that an expert with a quarter more than the average
+// needs.
+int expected_rounds(int pairs, int E, int most) {
+  return std::max(1, (5 * pairs / (4 * E) + most - 1) / most);
+}
+
+// `tiles` tiles of each expert, of `units` units of K and `columns` pairs at a
+// time. Where that leaves room for them, an expert's rounds are workgroups of
+// their own: up to four of those fit a CU (32 tokens, 4 experts of 2048 x
+// 1536, top 4: 384 workgroups 13.5 us, 768 11.4; 16 experts of 512 x 512, top
+// 8: 512 7.4 us, 1024 5.9; 8 experts of 1024 x 1440, top 8: 720 13.3 us, 1440
+// 14.1).
 template <class Kernel, class Args>
-hipError_t launch_tiles(Kernel kernel, int lds_per_wave, const Args& g, int64_t tiles,
+hipError_t launch_tiles(Kernel kernel, int columns, int lds_per_wave, const Args& g, int64_t tiles,
                         int64_t units, bool wave_tiles, const int32_t* ids, int pairs, int E,
                         hipStream_t stream) {
   const int waves = wave_tiles ? kTileWaves : even_waves((int)units, kTileWaves);
-  const dim3 grid(wave_tiles ? (tiles + kTileWaves - 1) / kTileWaves : tiles,
-                  pairs < E ? pairs : E);
+  const int chosen = pairs < E ? pairs : E;
+  const int64_t room = std::max<int64_t>(1, 1024 / (tiles * chosen));
+  const int rounds = (int)std::min<int64_t>(room, expected_rounds(pairs, E, columns));
+  const dim3 grid(wave_tiles ? (tiles + kTileWaves - 1) / kTileWaves : tiles, chosen,
+                  wave_tiles ? 1 : rounds);
   hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds_per_wave * waves, stream, g, ids, pairs,
                      E, pairs < E ? 1 : 0);
   return hipGetLastError();
@@ -511,15 +633,17 @@ hipError_t launch_pairs(const MoeArgs& m, hipStream_t stream) {
 
 hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   const int pairs = m.T * m.top_k, HB = m.H / 32, IB = m.I / 32, E = m.E;
-  // Workspace: the activations, then the pairs' parts of y.
-  float* act = m.workspace;
-  float* part = act + (int64_t)pairs * m.I;
+  // Workspace: the pairs' parts of y, then the activations' pieces.
+  const int pieces = m.out_fp32 ? 3 : 2;
+  float* part = m.workspace;
+  auto* act = reinterpret_cast<uint16_t*>(part + (int64_t)pairs * m.H);
   const int chosen = pairs < E ? pairs : E;
-  const UpArgs up = {m.x, m.ldx, m.w13, m.w13_s, act, HB, m.I, m.top_k};
+  const UpArgs up = {m.x, m.ldx, m.w13, m.w13_s, act, HB, m.I, m.top_k, pieces};
   const int64_t up_tiles = m.I / kFewTile, up_units = (HB + kUnitBlocks - 1) / kUnitBlocks;
   const bool up_waves = up_tiles * chosen >= kManyTiles;
-  const auto launch_up = [&](auto kernel, int lds) {
-    return launch_tiles(kernel, lds, up, up_tiles, up_units, up_waves, m.ids, pairs, E, stream);
+  const auto launch_up = [&](auto kernel, int columns, int lds) {
+    return launch_tiles(kernel, columns, lds, up, up_tiles, up_units, up_waves, m.ids, pairs, E,
+                        stream);
   };
   // Columns for up to 16 pairs in the first kernel, 8 in the second, cost
   // registers, and waves, where most experts have few: from 4 and 2 pairs an
@@ -529,29 +653,46 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   // 88.0 and 82.5).
   hipError_t e;
   if (pairs >= 4 * E)
-    e = launch_up(up_waves ? moe_up_kernel<4, true> : moe_up_kernel<4, false>,
+    e = launch_up(up_waves ? moe_up_kernel<4, true> : moe_up_kernel<4, false>, 16,
                   few_lds_bytes<2, BfRows<4>>());
   else
-    e = launch_up(up_waves ? moe_up_kernel<2, true> : moe_up_kernel<2, false>,
+    e = launch_up(up_waves ? moe_up_kernel<2, true> : moe_up_kernel<2, false>, 8,
                   few_lds_bytes<2, BfRows<2>>());
   if (e != hipSuccess) return e;
   const DownArgs down = {act, m.w2, m.w2_s, part, m.H, m.I};
   const int64_t down_tiles = m.H / (2 * kFewTile);
   const int64_t down_units = (IB + kUnitBlocks - 1) / kUnitBlocks;
   const bool down_waves = down_tiles * chosen >= kManyTiles;
-  const auto launch_down = [&](auto kernel, int lds) {
-    return launch_tiles(kernel, lds, down, down_tiles, down_units, down_waves, m.ids, pairs,
-                        E, stream);
+  const auto launch_down = [&](auto kernel, int columns, int lds) {
+    return launch_tiles(kernel, columns, lds, down, down_tiles, down_units, down_waves, m.ids,
+                        pairs, E, stream);
   };
-  if (m.out_fp32)
-    e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>,
-                    few_lds_bytes<2, F32Rows<4, 3>>());
+  // Many pairs an expert and few tiles, but a workgroup a CU: 32 tokens through
+  // all 8 experts of 1024 x 1440 10.0 us against 16.5 (12.0 with its rounds in
+  // workgroups of their own), 64 tokens, 8 experts of 4096 x 14336, top 2 124
+  // against 154, 32 experts of 1024 x 1024, 8 pairs each, 11.8 against 13.5.
+  // Fewer pairs (12 experts of 4096 x 1440, 4 each: 17.5 against 15.2), fewer
+  // workgroups (192: 15.7 against 12.4) or many tiles (128 experts of 2048 x
+  // 768, 8 each: 69.8 against 45) do not pay.
+  const int most = 32 / pieces;
+  const int64_t blocks = (m.H + kShareTiles * kFewTile - 1) / (kShareTiles * kFewTile);
+  const int rounds = std::min(8, expected_rounds(pairs, E, most));
+  if (pairs >= 8 * E && !down_waves && blocks * E * rounds >= 256) {
+    const int parts = IB > kUnitBlocks ? kDenseParts : 1;
+    const int lds = std::max(share_lds_bytes<4>(parts), share_lds_bytes<8>(parts));
+    hipLaunchKernelGGL(m.out_fp32 ? moe_dense_down_kernel<3> : moe_dense_down_kernel<2>,
+                       dim3(blocks, E, rounds), dim3(64 * kShareTiles * parts), lds, stream, down,
+                       m.ids, pairs, E);
+    e = hipGetLastError();
+  } else if (m.out_fp32)
+    e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>, 4,
+                    few_lds_bytes<2, DownRows<4, 3>>());
   else if (pairs >= 2 * E)
-    e = launch_down(down_waves ? moe_down_kernel<8, 2, true> : moe_down_kernel<8, 2, false>,
-                    few_lds_bytes<2, F32Rows<8, 2>>());
+    e = launch_down(down_waves ? moe_down_kernel<8, 2, true> : moe_down_kernel<8, 2, false>, 8,
+                    few_lds_bytes<2, DownRows<8, 2>>());
   else
-    e = launch_down(down_waves ? moe_down_kernel<4, 2, true> : moe_down_kernel<4, 2, false>,
-                    few_lds_bytes<2, F32Rows<4, 2>>());
+    e = launch_down(down_waves ? moe_down_kernel<4, 2, true> : moe_down_kernel<4, 2, false>, 4,
+                    few_lds_bytes<2, DownRows<4, 2>>());
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(m.out_fp32 ? moe_sum_kernel<true> : moe_sum_kernel<false>,
                      dim3((m.H / 2 + kSumThreads - 1) / kSumThreads, m.T), dim3(kSumThreads), 0,

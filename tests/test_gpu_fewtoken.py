@@ -334,6 +334,10 @@ def run_moe(x, ids, w, ex, **kw):
     # wave), and few experts of many pairs each.
     (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (20, 1024, 1152, 20, 3, 0.1), (40, 160, 288, 3, 2, 0.1),
     (64, 128, 96, 16, 8, 0.0), (100, 32, 32, 2, 1, 0.5),
+    # Many pairs an expert: waves that share the activations, one unit of K or
+    # less and several; H that leaves half a workgroup; rounds of workgroups.
+    (32, 736, 352, 8, 8, 0.0), (64, 992, 96, 8, 6, 0.3), (40, 1056, 800, 8, 5, 0.0),
+    (128, 2080, 160, 4, 4, 0.1), (32, 512, 512, 16, 8, 0.0),
 ])
 def test_moe_matches_the_oracle(T, H, I, E, k, absent, out):
     announce(f"moe T{T} H{H} I{I} E{E} k{k} absent {absent} {out}")
@@ -386,6 +390,30 @@ def test_moe_non_finite_tokens_stay_alone(T):
     assert torch.isnan(got[3]).all() and not torch.isfinite(got[5]).any()
 
 
+def test_moe_many_pairs_an_expert_with_tokens_not_finite():
+    """Non-finite tokens, an expert whose pairs are one token's many times, one
+    that is every token's, one of none; equal bits each time."""
+    announce("moe of many pairs, NaN and Inf tokens")
+    T, H, I, E, k = 48, 1120, 288, 8, 6
+    x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 1)
+    ex = experts(E, H, I, 5)
+    ids, w = choices(T, E, k, 6)
+    ids[:, 0] = 2
+    ids[ids == 7] = 2
+    ids[9] = 5
+    want, tol = fewtoken.moe(x, ids, w, *ex)
+    bad = x.copy()
+    bad[3, 10] = 0x7FC0                        # NaN
+    bad[40, :] = 0x7F00                        # 2^127: the activation overflows
+    rows = [t for t in range(T) if t not in (3, 40)]
+    for dt in (torch.float32, torch.bfloat16):
+        got = run_moe(bad, ids, w, ex, out_dtype=dt)
+        check(got[rows], want[rows], tol[rows])
+        assert torch.isnan(got[3]).all() and not torch.isfinite(got[40]).any()
+        for _ in range(3):
+            assert torch.equal(run_moe(bad, ids, w, ex, out_dtype=dt)[rows], got[rows])
+
+
 @pytest.mark.parametrize("T", [5, 11])
 def test_moe_strides_canaries_and_bits(T):
     """x rows strided among NaN, unaligned scales, canaries around y and the
@@ -414,7 +442,7 @@ def test_moe_strides_canaries_and_bits(T):
             assert torch.equal(mx.moe(*args, out_dtype=dt), out)
 
 
-@pytest.mark.parametrize("T,k,E", [(1, 6, 48), (3, 4, 48), (64, 6, 48), (64, 6, 8)])
+@pytest.mark.parametrize("T,k,E", [(1, 6, 48), (3, 4, 48), (64, 6, 48), (64, 6, 8), (100, 8, 10)])
 def test_moe_workspace_may_hold_anything(T, k, E):
     """A workspace of NaN, and absent experts whose part of it nothing writes."""
     announce(f"moe with a workspace of NaN, {T} tokens, {E} experts")

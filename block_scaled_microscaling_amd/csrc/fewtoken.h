@@ -286,7 +286,7 @@ __device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
 }
 
 // The next BF16 piece of v, which becomes its rest: FP32 holds it exactly, at
-// most 2^-9 of the value.
+// most 2^-8 of the value.
 __device__ __forceinline__ uint16_t next_piece(float& v) {
   const uint32_t bits = pack_bf16x2(v, v) << 16;
   // No rest where the piece is no finite number: inf - inf is NaN.

@@ -12,7 +12,7 @@
 //
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
 // once: HBM (1 token through 2 of 8 experts of 4096 x 14336, 187 MB, 22 + 16
-// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 41 + 26 + 5 us), or
+// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 42 + 25 + 5 us), or
 // latency where they are few (1 token through 8 of the latter, 5.2 + 4.7 us).
 //
 // Few pairs: as gemv's one-row kernel, in two launches. The first kernel's

@@ -6,7 +6,7 @@
 // all practical inputs), p = exp(l - max l) / sum exp(l - max l) in FP32.
 //
 // What bounds it: a few tokens' launches and latencies (1 token x 4096, 8
-// experts 3.9 us; 64 tokens x 4096, 128 experts 5.0 + 4.0), many tokens' 2 T E
+// experts 3.5 us; 64 tokens x 4096, 128 experts 5.0 + 4.0), many tokens' 2 T E
 // H flop of 64-bit arithmetic (512 tokens x 4096, 128 experts 20 us). The
 // bytes are few.
 //
@@ -24,8 +24,7 @@ namespace {
 typedef double v4d_t __attribute__((ext_vector_type(4)));
 
 constexpr int kOneWaves = 16;        // of the one-launch kernel
-constexpr int kOneExperts = 4;       // that a wave takes at once
-constexpr int kOneMaxExperts = 256;  // LDS: 16 partial sums of each
+constexpr int kOneMaxExperts = 128;  // 8 a wave
 constexpr int kTile = 16;            // tokens and experts of an MFMA
 constexpr int kTileWaves = 8;
 constexpr int kMaxSplits = 8;
@@ -143,51 +142,75 @@ __device__ __forceinline__ void choose(const double (&l)[kPerLane], int E, int t
   }
 }
 
-// One launch: the waves share the token's experts, four at a time, and, with
-// few experts, parts of H; wave 0 adds the parts and chooses.
+// Lane sums of four experts -> the total of expert r in lanes 16 r .. 16 r + 15.
+__device__ __forceinline__ double sum_four(const double (&v)[4]) {
+  const auto merge = [](double a, double b, auto swap) {
+    const uint64_t x = (uint64_t)__double_as_longlong(a), y = (uint64_t)__double_as_longlong(b);
+    const auto lo = swap((uint32_t)x, (uint32_t)y);
+    const auto hi = swap((uint32_t)(x >> 32), (uint32_t)(y >> 32));
+    return __longlong_as_double((int64_t)((uint64_t)hi[0] << 32 | lo[0])) +
+           __longlong_as_double((int64_t)((uint64_t)hi[1] << 32 | lo[1]));
+  };
+  const auto swap32 = [](uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  };
+  const auto swap16 = [](uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  };
+  double s = merge(merge(v[0], v[2], swap32), merge(v[1], v[3], swap32), swap16);
+  const auto add = [](double a, uint64_t b) { return a + __longlong_as_double((int64_t)b); };
+  s = add(s, dpp64<0xB1>((uint64_t)__double_as_longlong(s)));
+  s = add(s, dpp64<0x4E>((uint64_t)__double_as_longlong(s)));
+  s = add(s, dpp64<0x141>((uint64_t)__double_as_longlong(s)));
+  return add(s, dpp64<0x140>((uint64_t)__double_as_longlong(s)));
+}
+
+// One launch: each wave takes 4 kPerLane of the token's experts or, with few
+// experts, a part of H for them; wave 0 adds the parts and chooses. So every
+// wave's loads go out at once (7 tokens x 296, 120 experts: four experts after
+// four 8.2 us a call, all at once 6.3), and four sums are reduced as one (7
+// tokens x 920, 7 experts 4.5 -> 3.7 us).
 template <int kPerLane>
 __global__ __launch_bounds__(64 * kOneWaves) void route_one_kernel(
     const uint8_t* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ router, int H, int E,
     int top_k, int renormalize, int32_t* __restrict__ ids, float* __restrict__ weights) {
-  __shared__ double part[kOneWaves * kOneExperts > kOneMaxExperts ? kOneWaves * kOneExperts
-                                                                  : kOneMaxExperts];
+  constexpr int kExperts = 4 * kPerLane;
+  __shared__ double part[kOneWaves * kExperts];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int groups = (E + kOneExperts - 1) / kOneExperts;
-  const int parts = groups < kOneWaves ? kOneWaves / groups : 1;
+  const int groups = (E + kExperts - 1) / kExperts;
+  const int parts = kOneWaves / groups;
   const int64_t t = blockIdx.x;
   const auto* xr = reinterpret_cast<const u32x4_t*>(x + t * ldx * 2);
-  for (int item = wave; item < groups * parts; item += kOneWaves) {
-    const int group = item / parts, p = item - group * parts;
-    double sum[kOneExperts] = {};
+  const int group = wave / parts, p = wave - group * parts;
+  if (group < groups) {
+    double sum[kPerLane][4] = {};
     for (int i = p * 64 + lane; i < H / 8; i += parts * 64) {
       const u32x4_t a = xr[i];
-      u32x4_t b[kOneExperts];
+      u32x4_t b[kPerLane][4];
 #pragma unroll
-      for (int n = 0; n < kOneExperts; ++n) {
-        const int e = min(group * kOneExperts + n, E - 1);
-        b[n] = reinterpret_cast<const u32x4_t*>(router + (int64_t)e * H * 2)[i];
+      for (int n = 0; n < kExperts; ++n) {
+        const int e = min(group * kExperts + n, E - 1);
+        b[n / 4][n % 4] = reinterpret_cast<const u32x4_t*>(router + (int64_t)e * H * 2)[i];
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t aw = a[q];
         const double a0 = lo_bf16(aw), a1 = hi_bf16(aw);
 #pragma unroll
-        for (int n = 0; n < kOneExperts; ++n) {
-          const uint32_t bw = b[n][q];
-          sum[n] = fma(a0, lo_bf16(bw), sum[n]);
-          sum[n] = fma(a1, hi_bf16(bw), sum[n]);
+        for (int n = 0; n < kExperts; ++n) {
+          const uint32_t bw = b[n / 4][n % 4][q];
+          double& s = sum[n / 4][n % 4];
+          s = fma(a0, lo_bf16(bw), s);
+          s = fma(a1, hi_bf16(bw), s);
         }
       }
     }
 #pragma unroll
-    for (int n = 0; n < kOneExperts; ++n) sum[n] = wave_sum(sum[n]);
-    if (lane == 0) {
-#pragma unroll
-      for (int n = 0; n < kOneExperts; ++n) {
-        const int e = group * kOneExperts + n;
-        if (e < E) part[p * E + e] = sum[n];
-      }
+    for (int n = 0; n < kPerLane; ++n) {
+      const double s = sum_four(sum[n]);
+      const int e = group * kExperts + 4 * n + (lane >> 4);
+      if ((lane & 15) == 0 && e < E) part[p * E + e] = s;
     }
   }
   __syncthreads();
@@ -282,10 +305,12 @@ hipError_t launch_top(const double* logits, int T, int E, int top_k, int renorma
 }
 
 // One workgroup a token does all of 64-bit arithmetic on one CU: up to 64 Ki
-// products and a token a CU that is no slower than the tiles (16 tokens x
-// 4096, 8 and 16 experts 6.4 and 7.4 us against 7.2 and 7.6; 32 experts 9.1
-// against 7.7; 512 tokens x 1024, 32 experts 8.9 against 7.6) and saves the
-// host a launch.
+// products and a token a CU that is no slower than the tiles (51 tokens x 800,
+// 87 experts, 70 Ki, 5.9 us against 6.2; 1 x 2240, 34 experts, 76 Ki, 7.2
+// against 6.7; 14 x 1680, 128 experts, 215 Ki, 10.3 against 6.3; 512 tokens x
+// 1024, 32 experts 8.9 against 7.6) and saves the host a launch. Past 128
+// experts a wave's loads no longer fit its registers (2 tokens x 264, 180
+// experts 8.0 us in one launch, 6.5 in two).
 bool one_launch(int64_t T, int64_t H, int64_t E) {
   return E <= kOneMaxExperts && E * H <= 65536 && T <= 256;
 }
@@ -314,7 +339,7 @@ hipError_t launch_moe_route(const void* x, int64_t ldx, const void* router, int 
   const auto* rb = static_cast<const uint8_t*>(router);
   const int renorm = renormalize ? 1 : 0;
   if (one_launch(T, H, E)) {
-    hipLaunchKernelGGL(E <= 64 ? route_one_kernel<1> : route_one_kernel<4>, dim3(T),
+    hipLaunchKernelGGL(E <= 64 ? route_one_kernel<1> : route_one_kernel<2>, dim3(T),
                        dim3(64 * kOneWaves), 0, stream, xb, ldx, rb, H, E, top_k, renorm, ids,
                        weights);
     return hipGetLastError();

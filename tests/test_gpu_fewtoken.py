@@ -235,7 +235,8 @@ def test_gemv_with_more_rows_than_a_grid_has_threads():
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("T,H,E,k", [
     (1, 8, 1, 1), (1, 4096, 8, 2), (3, 24, 5, 5), (7, 520, 61, 4), (9, 2856, 64, 8),
-    (17, 1000, 65, 1), (33, 64, 200, 32), (64, 2048, 128, 8), (2, 512, 1024, 32), (100, 72, 256, 6),
+    (17, 1000, 65, 1), (33, 64, 200, 32), (3, 296, 127, 9), (5, 512, 128, 4),
+    (4, 72, 129, 3), (64, 2048, 128, 8), (2, 512, 1024, 32), (100, 72, 256, 6),
 ])
 def test_route_matches_the_oracle(T, H, E, k, renorm):
     announce(f"route {T}x{H} {E} top {k} renorm {renorm}")
@@ -332,7 +333,8 @@ def run_moe(x, ids, w, ex, **kw):
     (1, 96, 224, 40, 32, 0.5),
     # By experts: fewer pairs than experts (K split over waves, and a tile a
     # wave), and few experts of many pairs each.
-    (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (20, 1024, 1152, 20, 3, 0.1), (40, 160, 288, 3, 2, 0.1),
+    (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (20, 1024, 1152, 20, 3, 0.1),
+    (40, 160, 288, 3, 2, 0.1),
     (64, 128, 96, 16, 8, 0.0), (100, 32, 32, 2, 1, 0.5),
     # Many pairs an expert: waves that share the activations, one unit of K or
     # less and several; H that leaves half a workgroup; rounds of workgroups.

@@ -42,18 +42,17 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // ------------------------------------------------------ one activation row
-// Lane sums of four rows -> the row r's total in lanes 16 r .. 16 r + 15.
-__device__ __forceinline__ float sum_four_rows(const float (&v)[4]) {
-  const auto merge32 = [](float a, float b) {  // low half: a's, high half: b's
-    const auto s =
-        __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  };
-  const float a = merge32(v[0], v[2]), b = merge32(v[1], v[3]);
+// Sums of two values over pairs of 16 lanes: a's in the even ones, b's in the
+// odd ones.
+__device__ __forceinline__ float merge16(float a, float b) {
   const auto s =
       __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-  float sum = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  const auto rotated = [](float f, auto ctrl) {  // within 16 lanes
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// The sum over each 16 lanes, in all of them.
+__device__ __forceinline__ float sum16(float sum) {
+  const auto rotated = [](float f, auto ctrl) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
         0, (int)__float_as_uint(f), decltype(ctrl)::value, 0xF, 0xF, false));
   };
@@ -63,6 +62,21 @@ __device__ __forceinline__ float sum_four_rows(const float (&v)[4]) {
   sum += rotated(sum, std::integral_constant<int, 0x121>{});
   return sum;
 }
+
+// Lane sums of four rows -> the row r's total in lanes 16 r .. 16 r + 15.
+__device__ __forceinline__ float sum_four_rows(const float (&v)[4]) {
+  const auto merge32 = [](float a, float b) {  // low half: a's, high half: b's
+    const auto s =
+        __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  };
+  return sum16(merge16(merge32(v[0], v[2]), merge32(v[1], v[3])));
+}
+
+// Short rows, of up to kLanes (16, 32 or 64) blocks: a wave takes 64 / kLanes
+// rows at a time, so that its lanes have work, and a workgroup is four waves
+// that need nothing of each other.
+constexpr int kShortWaves = 4;
 
 // acc + the product of a block's 32 codes with 32 BF16 activations.
 __device__ __forceinline__ float dot_block(u32x4_t w, float scale, const u32x4_t (&x)[4],

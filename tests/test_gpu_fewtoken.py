@@ -68,6 +68,8 @@ def test_gemv_decodes_every_code_and_scale_exactly(M):
     # Enough tiles for two a workgroup; one row over many rounds of K.
     (3, 5000, 352), (5, 6177, 736), (16, 6200, 544), (40, 4001, 96), (2, 24, 32), (1, 9, 33024),
     (6, 40, 33024),
+    # One row of up to 16, 32 and 64 blocks, and tails.
+    (1, 1000, 512), (1, 77, 544), (1, 333, 1024), (1, 1029, 1056), (1, 30, 2048), (1, 31, 2080),
     # Enough workgroups for their waves to share x: one unit of K, odd ones.
     (6, 14400, 256), (5, 14341, 800), (16, 14337, 4128), (50, 3600, 288), (9, 20000, 544),
 ])
@@ -336,6 +338,9 @@ def run_moe(x, ids, w, ex, **kw):
     (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (20, 1024, 1152, 20, 3, 0.1),
     (40, 160, 288, 3, 2, 0.1),
     (64, 128, 96, 16, 8, 0.0), (100, 32, 32, 2, 1, 0.5),
+    # By pairs: up to 16, 32 and 64 blocks of H.
+    (3, 512, 96, 20, 4, 0.1), (2, 544, 32, 12, 3, 0.0), (1, 1024, 64, 6, 5, 0.2),
+    (2, 1056, 32, 16, 4, 0.0), (1, 2048, 96, 8, 4, 0.0), (1, 2080, 64, 8, 4, 0.3),
     # Many pairs an expert: waves that share the activations, one unit of K or
     # less and several; H that leaves half a workgroup; rounds of workgroups.
     (32, 736, 352, 8, 8, 0.0), (64, 992, 96, 8, 6, 0.3), (40, 1056, 800, 8, 5, 0.0),

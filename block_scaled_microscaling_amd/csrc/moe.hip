@@ -245,18 +245,6 @@ __device__ __forceinline__ int list_pairs(const int32_t* ids, int pairs, int e, 
   return n;
 }
 
-// The pairs of the workgroup's expert, in LDS, and how many; e is the expert.
-// With fewer pairs than experts the grid's y counts pairs, and the first pair
-// of an expert stands for all of them; otherwise it counts experts. Every
-// wave writes the same list.
-__device__ __forceinline__ int expert_pairs(const int32_t* __restrict__ ids, int pairs, int E,
-                                            int by_pair, uint16_t* list, int& e) {
-  e = by_pair ? ids[blockIdx.y] : (int)blockIdx.y;
-  if (e < 0 || e >= E) return 0;
-  const int n = list_pairs(ids, pairs, e, list);
-  return by_pair && n > 0 && list[0] != blockIdx.y ? 0 : n;
-}
-
 // Products of two tiles of 16 weight rows, at the uniform rows row0 and row1,
 // with X's columns, K split over the workgroup's waves; the results are left
 // in LDS, for tile_sum.
@@ -367,13 +355,12 @@ __device__ __forceinline__ void up_wave(const UpArgs& g, int64_t gate, int i0,
 // A workgroup takes 16 activation columns of an expert, or, with kWaveTiles,
 // each of its waves does.
 template <int kMaxXL, bool kWaveTiles>
-__global__ __launch_bounds__(64 * kTileWaves) void moe_up_kernel(UpArgs g,
-                                                                 const int32_t* __restrict__ ids,
-                                                                 int pairs, int E, int by_pair) {
+__global__ __launch_bounds__(64 * kTileWaves) void moe_up_kernel(
+    UpArgs g, const int32_t* __restrict__ ids, int pairs) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[kMaxPairs];
-  int e;
-  const int n = expert_pairs(ids, pairs, E, by_pair, list, e);
+  const int e = blockIdx.y;
+  const int n = list_pairs(ids, pairs, e, list);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i0 = (kWaveTiles ? blockIdx.x * kTileWaves + wave : blockIdx.x) * kFewTile;
   if (n == 0 || i0 >= g.I) return;
@@ -480,11 +467,11 @@ __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0
 // waves does.
 template <int kMaxRows, int kPieces, bool kWaveTiles>
 __global__ __launch_bounds__(64 * kTileWaves) void moe_down_kernel(
-    DownArgs g, const int32_t* __restrict__ ids, int pairs, int E, int by_pair) {
+    DownArgs g, const int32_t* __restrict__ ids, int pairs) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[kMaxPairs];
-  int e;
-  const int n = expert_pairs(ids, pairs, E, by_pair, list, e);
+  const int e = blockIdx.y;
+  const int n = list_pairs(ids, pairs, e, list);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int h0 = (kWaveTiles ? blockIdx.x * kTileWaves + wave : blockIdx.x) * 2 * kFewTile;
   if (n == 0 || h0 >= g.H) return;
@@ -534,7 +521,7 @@ __device__ __forceinline__ float share_get(const uint8_t* lds, int tile, int r, 
 // weight is decoded once for two products.
 template <int kPieces>
 __global__ __launch_bounds__(64 * kShareTiles * kDenseParts) void moe_dense_down_kernel(
-    DownArgs g, const int32_t* __restrict__ ids, int pairs, int E) {
+    DownArgs g, const int32_t* __restrict__ ids, int pairs) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[kMaxPairs];
   const int e = blockIdx.y;
@@ -638,28 +625,31 @@ hipError_t launch_tiles(Kernel kernel, int columns, int lds_per_wave, const Args
                         int64_t units, bool wave_tiles, const int32_t* ids, int pairs, int E,
                         hipStream_t stream) {
   const int waves = wave_tiles ? kTileWaves : even_waves((int)units, kTileWaves);
-  const int chosen = pairs < E ? pairs : E;
-  const int64_t room = std::max<int64_t>(1, 1024 / (tiles * chosen));
+  const int64_t room = std::max<int64_t>(1, 1024 / (tiles * E));
   const int rounds = (int)std::min<int64_t>(room, expected_rounds(pairs, E, columns));
-  const dim3 grid(wave_tiles ? (tiles + kTileWaves - 1) / kTileWaves : tiles, chosen,
+  const dim3 grid(wave_tiles ? (tiles + kTileWaves - 1) / kTileWaves : tiles, E,
                   wave_tiles ? 1 : rounds);
-  hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds_per_wave * waves, stream, g, ids, pairs,
-                     E, pairs < E ? 1 : 0);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds_per_wave * waves, stream, g, ids,
+                     pairs);
   return hipGetLastError();
 }
 
 // Whether every pair reads its expert's weights for itself. One token's
-// experts differ anyway; several tokens seldom share one while there are
-// fewer pairs than 3/4 of the experts (128 experts of 2048 x 768, top 8: 2
-// tokens 12.8 us against 17.2 by experts, 8 tokens 31.6 against 34.6, 16
-// tokens 53.9 against 53.1). With up to four pairs an expert that together
-// read up to 32 MiB the caches serve them and the launch less counts (7
-// tokens, 10 experts of 1056 x 544, top 3: 9.4 against 11.9 us; 16 tokens,
-// 44 MB, 13.7 against 13.4).
+// experts differ anyway, and several tokens seldom share one while there are
+// fewer pairs than experts (128 experts of 2048 x 768, top 8: 2 tokens 12.8 us
+// against 17.2 by experts, 8 tokens 31.6 against 34.6, 16 tokens 53.6 and 53.6,
+// 24 tokens 72.8 against 62.2). The less the pairs read, the better the caches
+// serve what they share, and the launch less counts: up to 1.5 pairs an expert
+// with 256 MiB (5 x 480 x 4640, 17 experts, top 3, 53 MB, 14.9 against 20.1; 8
+// x 4096 x 1440, 12 top 2, 150 MB, 26.0 and 25.9; 4 x 4096 x 14336, 8 top 2,
+// 749 MB, 124.8 against 109.4), up to four with 64 MiB (31 x 352 x 576, 76 top
+// 6, 60 MB, 15.5 against 18.3; 14 x 1792 x 576, 16 top 4, 92 MB, 19.4 against
+// 16.4).
 bool by_pairs(int T, int H, int I, int E, int top_k) {
-  const int64_t pairs = (int64_t)T * top_k;
-  return T == 1 || 4 * pairs <= 3 * (int64_t)E ||
-         (pairs <= 4 * (int64_t)E && pairs * 3 * H * I / 32 * 17 <= (int64_t)32 << 20);
+  const int64_t pairs = (int64_t)T * top_k, bytes = pairs * 3 * H * I / 32 * 17;
+  return T == 1 || pairs < E ||
+         (2 * pairs <= 3 * (int64_t)E && bytes <= (int64_t)256 << 20) ||
+         (pairs <= 4 * (int64_t)E && bytes <= (int64_t)64 << 20);
 }
 
 // What a call of moe works on.
@@ -701,10 +691,9 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   const int pieces = m.out_fp32 ? 3 : 2;
   float* part = m.workspace;
   auto* act = reinterpret_cast<uint16_t*>(part + (int64_t)pairs * m.H);
-  const int chosen = pairs < E ? pairs : E;
   const UpArgs up = {m.x, m.ldx, m.w13, m.w13_s, act, HB, m.I, m.top_k, pieces};
   const int64_t up_tiles = m.I / kFewTile, up_units = (HB + kUnitBlocks - 1) / kUnitBlocks;
-  const bool up_waves = up_tiles * chosen >= kManyTiles;
+  const bool up_waves = up_tiles * E >= kManyTiles;
   const auto launch_up = [&](auto kernel, int columns, int lds) {
     return launch_tiles(kernel, columns, lds, up, up_tiles, up_units, up_waves, m.ids, pairs, E,
                         stream);
@@ -726,7 +715,7 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   const DownArgs down = {act, m.w2, m.w2_s, part, m.H, m.I};
   const int64_t down_tiles = m.H / (2 * kFewTile);
   const int64_t down_units = (IB + kUnitBlocks - 1) / kUnitBlocks;
-  const bool down_waves = down_tiles * chosen >= kManyTiles;
+  const bool down_waves = down_tiles * E >= kManyTiles;
   const auto launch_down = [&](auto kernel, int columns, int lds) {
     return launch_tiles(kernel, columns, lds, down, down_tiles, down_units, down_waves, m.ids,
                         pairs, E, stream);
@@ -746,7 +735,7 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
     const int lds = std::max(share_lds_bytes<4>(parts), share_lds_bytes<8>(parts));
     hipLaunchKernelGGL(m.out_fp32 ? moe_dense_down_kernel<3> : moe_dense_down_kernel<2>,
                        dim3(blocks, E, rounds), dim3(64 * kShareTiles * parts), lds, stream, down,
-                       m.ids, pairs, E);
+                       m.ids, pairs);
     e = hipGetLastError();
   } else if (m.out_fp32)
     e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>, 4,

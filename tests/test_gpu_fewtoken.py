@@ -333,9 +333,11 @@ def run_moe(x, ids, w, ex, **kw):
     # experts, and tiles that fill no workgroup.
     (128, 1024, 512, 64, 8, 0.1), (16, 288, 288, 1000, 16, 0.2), (2, 160, 1056, 9, 9, 0.3),
     (1, 96, 224, 40, 32, 0.5),
-    # By experts: fewer pairs than experts (K split over waves, and a tile a
-    # wave), and few experts of many pairs each.
+    # Fewer pairs than experts with many bytes; by experts: up to two pairs an
+    # expert (K split over waves, and a tile a wave), and more.
     (6, 1024, 1152, 20, 3, 0.1), (6, 3680, 1856, 20, 3, 0.0), (20, 1024, 1152, 20, 3, 0.1),
+    (5, 1696, 4640, 6, 2, 0.0), (14, 1120, 1760, 24, 3, 0.1), (9, 3648, 2240, 14, 2, 0.0),
+    (40, 1024, 512, 64, 4, 0.0), (28, 1024, 512, 64, 4, 0.1), (64, 288, 544, 64, 5, 0.0),
     (40, 160, 288, 3, 2, 0.1),
     (64, 128, 96, 16, 8, 0.0), (100, 32, 32, 2, 1, 0.5),
     # By pairs: up to 16, 32 and 64 blocks of H.

@@ -6,8 +6,8 @@
 //
 // What bounds it: the weight's 17/32 byte per element, read once, for 2 M flop
 // per element: HBM; from about 8 rows on also the re-reads of x from L2, once
-// a workgroup. 1 x 8192 x 8192 8.1 us (4.4 TB/s), 8 x 4096 x 14336 8.9 us, 16
-// x 28672 x 4096 17.4 us, 1 x 28672 x 4096 11.0 us (5.7 TB/s).
+// a workgroup. 1 x 8192 x 8192 8.0 us (4.5 TB/s), 8 x 4096 x 14336 9.2 us, 16
+// x 28672 x 4096 15.5 us, 1 x 28672 x 4096 11.0 us (5.7 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

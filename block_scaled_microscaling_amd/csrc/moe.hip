@@ -12,8 +12,8 @@
 //
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
 // once: HBM (1 token through 2 of 8 experts of 4096 x 14336, 187 MB, 22 + 16
-// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 42 + 25 + 5 us), or
-// latency where they are few (1 token through 8 of the latter, 5.2 + 4.7 us).
+// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 41 + 25 + 5 us), or
+// latency where they are few (1 token through 8 of the latter, 4.9 + 4.8 us).
 //
 // Few pairs: as gemv's one-row kernel, in two launches. The first kernel's
 // workgroup has two gate and two up rows of a pair's expert; the second's

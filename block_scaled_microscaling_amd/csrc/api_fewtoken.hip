@@ -95,8 +95,8 @@ int mxfp4_moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top_k, int64_t*
     return MXFP4_EINVAL;
   if (H < 32 || H % 32 != 0 || H > kMaxMoeDim || I < 32 || I % 32 != 0 || I > kMaxMoeDim)
     return MXFP4_EINVAL;
-  // One token: the pairs' activations, FP32. Several: up to three BF16 pieces
-  // of the activations and the pairs' parts of y, FP32.
+  // One token: the pairs' activations, FP32. Several: three BF16 pieces of the
+  // activations and the pairs' parts of y, FP32.
   *bytes = T * top_k * (T > 1 ? 6 * I + 4 * H : 4 * I);
   return MXFP4_OK;
 }

@@ -5,14 +5,16 @@
 //   a[p, i] = silu(sum_h Wg_e[i, h] x[t, h]) * (sum_h Wu_e[i, h] x[t, h])
 //   y[t, h] = sum_j weights[t, j] sum_i W2_e[h, i] a[p, i]
 // Weights are exact in BF16, sums and a are FP32. The second product takes a
-// as FP32 (by pairs) or as the sum of BF16 pieces in columns of the same
-// MFMA: three, all of FP32's significand, for FP32 results; two, 16 bits, for
-// BF16 results, whose own rounding is 2^8 times larger. The first kernel by
-// experts writes the pieces, so that they are made once.
+// as FP32 (by pairs) or as the sum of three BF16 pieces, all of FP32's
+// significand, in columns of the same MFMA, so that what a token gets does not
+// depend on which of the two the batch beside it takes. Two pieces, 16 bits,
+// are 5 to 20% faster but change 0.2% of BF16 results by a step, and all that
+// is left of large activations that cancel. The first kernel by experts writes
+// the pieces, so that they are made once.
 //
 // What bounds it: the chosen experts' weights, 3 H I 17/32 bytes each, read
 // once: HBM (1 token through 2 of 8 experts of 4096 x 14336, 187 MB, 22 + 16
-// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 41 + 25 + 5 us), or
+// us; 32 tokens through 112 of 128 of 2048 x 768, 281 MB, 73 us), or
 // latency where they are few (1 token through 8 of the latter, 4.9 + 4.8 us).
 //
 // Few pairs: as gemv's one-row kernel, in two launches. The first kernel's
@@ -37,6 +39,8 @@ constexpr int kPairDownWaves = 7;  // 63 KiB of LDS
 constexpr int kMaxPairs = 1024;
 constexpr int kTileWaves = 4;   // of the kernels for several tokens
 constexpr int kDenseParts = 2;  // parts of K of the kernel for many pairs an expert
+constexpr int kPieces = 3;      // BF16 pieces of an activation
+constexpr int kDownRows = 4;    // pairs of the second kernel by experts: 12 columns
 
 template <bool kOutFp32>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
@@ -285,8 +289,8 @@ struct UpArgs {
   int64_t ldx;
   const uint8_t* w13;
   const uint8_t* w13_s;
-  uint16_t* act;  // [pairs][I / 16][pieces][16]: BF16 pieces of the activations
-  int HB, I, top_k, pieces;
+  uint16_t* act;  // [pairs][I / 16][kPieces][16]: BF16 pieces of the activations
+  int HB, I, top_k;
 };
 
 // The tokens of the pairs list[p0 .. p0 + 4 XL); past the n-th, of the last.
@@ -316,8 +320,9 @@ __device__ __forceinline__ void up_tile(const UpArgs& g, int64_t gate, int i0,
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       v[j] = silu_mul(tile_sum(lds, 0, r + j, c), tile_sum(lds, 1, r + j, c));
-    uint16_t* at = g.act + ((int64_t)list[p0 + c] * g.I + i0) * g.pieces + r;
-    for (int piece = 0; piece < g.pieces; ++piece, at += kFewTile) {
+    uint16_t* at = g.act + ((int64_t)list[p0 + c] * g.I + i0) * kPieces + r;
+#pragma unroll
+    for (int piece = 0; piece < kPieces; ++piece, at += kFewTile) {
       const uint32_t low = next_piece(v[0]);
       *reinterpret_cast<uint32_t*>(at) = low | (uint32_t)next_piece(v[1]) << 16;
     }
@@ -338,8 +343,9 @@ __device__ __forceinline__ void up_wave(const UpArgs& g, int64_t gate, int i0,
   v4f_t v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = silu_mul(acc[0][i], acc[1][i]);
-  uint16_t* at = g.act + ((int64_t)list[p0 + c] * g.I + i0) * g.pieces + 4 * (lane >> 4);
-  for (int piece = 0; piece < g.pieces; ++piece, at += kFewTile) {
+  uint16_t* at = g.act + ((int64_t)list[p0 + c] * g.I + i0) * kPieces + 4 * (lane >> 4);
+#pragma unroll
+  for (int piece = 0; piece < kPieces; ++piece, at += kFewTile) {
     uint16_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -393,51 +399,44 @@ struct DownArgs {
 };
 
 // The lane's place in the first block of a pair's piece.
-template <int kPieces>
 __device__ __forceinline__ const uint8_t* piece_at(const DownArgs& g, int p, int piece) {
   const int q = threadIdx.x & 3;
   return reinterpret_cast<const uint8_t*>(
       g.act + (int64_t)p * g.I * kPieces + ((q >> 1) * kPieces + piece) * kFewTile + (q & 1) * 8);
 }
 
-// The pieces of the pairs list[p0 .. p0 + kRows), a piece of all of them after
-// the other; past the n-th pair, of the last.
-template <int kRows, int kPieces>
-using DownRows = BfRows<kRows * kPieces / 4, 64 * kPieces>;
+// The pieces of the pairs list[p0 .. p0 + kDownRows), a piece of all of them
+// after the other; past the n-th pair, of the last.
+using DownRows = BfRows<kDownRows * kPieces / 4, 64 * kPieces>;
+static_assert(kDownRows == 4, "a load of BfRows is one piece of the pairs");
 
-template <int kRows, int kPieces>
-__device__ __forceinline__ DownRows<kRows, kPieces> down_rows(const DownArgs& g,
-                                                              const uint16_t* list, int p0,
-                                                              int n) {
-  DownRows<kRows, kPieces> rows;
+__device__ __forceinline__ DownRows down_rows(const DownArgs& g, const uint16_t* list, int p0,
+                                              int n) {
+  DownRows rows;
+  const int c = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int i = 0; i < kRows * kPieces / 4; ++i) {
-    const int c = 4 * i + ((threadIdx.x & 63) >> 4);
-    rows.p[i] = piece_at<kPieces>(g, list[min(p0 + c % kRows, n - 1)], c / kRows);
-  }
+  for (int piece = 0; piece < kPieces; ++piece)
+    rows.p[piece] = piece_at(g, list[min(p0 + c, n - 1)], piece);
   return rows;
 }
 
-// Outputs h0 .. h0 + 31 of the pairs list[p0 .. p0 + kRows), K split over the
-// waves.
-template <int kRows, int kPieces>
+// Outputs h0 .. h0 + 31 of the pairs list[p0 .. p0 + kDownRows), K split over
+// the waves.
 __device__ __forceinline__ void down_tile(const DownArgs& g, int64_t row, int h0,
                                           const uint16_t* list, int p0, int n, uint8_t* lds) {
-  two_tiles(g.w2, g.w2_s, row, row + kFewTile, g.I / 32,
-            down_rows<kRows, kPieces>(g, list, p0, n), lds);
-  for (int i = threadIdx.x; i < 32 * kRows; i += blockDim.x) {
+  two_tiles(g.w2, g.w2_s, row, row + kFewTile, g.I / 32, down_rows(g, list, p0, n), lds);
+  for (int i = threadIdx.x; i < 32 * kDownRows; i += blockDim.x) {
     const int r = i & 31, c = i >> 5;
     if (p0 + c >= n) continue;
     float sum = 0.0f;
 #pragma unroll
     for (int piece = kPieces - 1; piece >= 0; --piece)
-      sum += tile_sum(lds, r >> 4, r & 15, piece * kRows + c);
+      sum += tile_sum(lds, r >> 4, r & 15, piece * kDownRows + c);
     g.part[(int64_t)list[p0 + c] * g.H + h0 + r] = sum;
   }
 }
 
 // The same with a tile a wave, over all of I.
-template <int kRows, int kPieces>
 __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0,
                                           const uint16_t* list, int p0, int n, uint8_t* lds) {
   const int lane = threadIdx.x & 63, c = lane & 15;
@@ -445,19 +444,19 @@ __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0
   const uint8_t* wc[2] = {g.w2 + row * IB * 16, g.w2 + (row + kFewTile) * IB * 16};
   const uint8_t* ws[2] = {g.w2_s + row * IB, g.w2_s + (row + kFewTile) * IB};
   v4f_t acc[2] = {v4f_t{}, v4f_t{}};
-  few_stream<2, true>(wc, ws, [](int, int r) { return r; },
-                      down_rows<kRows, kPieces>(g, list, p0, n), IB, 0, 1, lds, acc);
+  few_stream<2, true>(wc, ws, [](int, int r) { return r; }, down_rows(g, list, p0, n), IB, 0, 1,
+                      lds, acc);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     // The sum of the pieces' columns.
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float sum = c < kRows * kPieces ? acc[t][i] : 0.0f;
-      sum += __shfl_xor(sum, kRows);
-      if (kPieces == 3) sum += __shfl_xor(sum, 2 * kRows);
+      float sum = c < kDownRows * kPieces ? acc[t][i] : 0.0f;
+      sum += __shfl_xor(sum, kDownRows);
+      sum += __shfl_xor(sum, 2 * kDownRows);
       acc[t][i] = sum;
     }
-    if (c < kRows && p0 + c < n)
+    if (c < kDownRows && p0 + c < n)
       *reinterpret_cast<v4f_t*>(g.part + (int64_t)list[p0 + c] * g.H + h0 + t * kFewTile +
                                 4 * (lane >> 4)) = acc[t];
   }
@@ -465,7 +464,7 @@ __device__ __forceinline__ void down_wave(const DownArgs& g, int64_t row, int h0
 
 // A workgroup takes 32 outputs of an expert, or, with kWaveTiles, each of its
 // waves does.
-template <int kMaxRows, int kPieces, bool kWaveTiles>
+template <bool kWaveTiles>
 __global__ __launch_bounds__(64 * kTileWaves) void moe_down_kernel(
     DownArgs g, const int32_t* __restrict__ ids, int pairs) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -476,19 +475,11 @@ __global__ __launch_bounds__(64 * kTileWaves) void moe_down_kernel(
   const int h0 = (kWaveTiles ? blockIdx.x * kTileWaves + wave : blockIdx.x) * 2 * kFewTile;
   if (n == 0 || h0 >= g.H) return;
   const int64_t row = (int64_t)e * g.H + h0;
-  uint8_t* mine = lds + wave * few_lds_bytes<2, DownRows<kMaxRows, kPieces>>();
-  const auto take = [&](auto r, int p0) {
-    constexpr int kRows = decltype(r)::value;
+  for (int p0 = blockIdx.z * kDownRows; p0 < n; p0 += gridDim.z * kDownRows) {
     if constexpr (kWaveTiles)
-      down_wave<kRows, kPieces>(g, row, h0, list, p0, n, mine);
+      down_wave(g, row, h0, list, p0, n, lds + wave * few_lds_bytes<2, DownRows>());
     else
-      down_tile<kRows, kPieces>(g, row, h0, list, p0, n, lds);
-  };
-  for (int p0 = blockIdx.z * kMaxRows; p0 < n; p0 += gridDim.z * kMaxRows) {
-    if (kMaxRows > 4 && n - p0 <= 4)
-      take(std::integral_constant<int, 4>{}, p0);
-    else
-      take(std::integral_constant<int, kMaxRows>{}, p0);
+      down_tile(g, row, h0, list, p0, n, lds);
   }
 }
 
@@ -517,9 +508,10 @@ __device__ __forceinline__ float share_get(const uint8_t* lds, int tile, int r, 
 }
 
 // Many pairs an expert. A workgroup takes 64 outputs of an expert and its waves
-// share the pieces of 16 pairs (10 if three pieces), or of half as many, so a
-// weight is decoded once for two products.
-template <int kPieces>
+// share the pieces of 10 pairs, or of 5, so a weight is decoded once for two
+// products.
+constexpr int kDensePairs = 32 / kPieces;
+
 __global__ __launch_bounds__(64 * kShareTiles * kDenseParts) void moe_dense_down_kernel(
     DownArgs g, const int32_t* __restrict__ ids, int pairs) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -540,8 +532,7 @@ __global__ __launch_bounds__(64 * kShareTiles * kDenseParts) void moe_dense_down
         g.w2 + row * IB * 16, g.w2_s + row * IB,
         [&](int r) { return min(kFewTile * tile + r, last); },
         [&](int c) {
-          return piece_at<kPieces>(g, list[min(p0 + c % kRows, n - 1)],
-                                   min(c / kRows, kPieces - 1));
+          return piece_at(g, list[min(p0 + c % kRows, n - 1)], min(c / kRows, kPieces - 1));
         },
         IB, tile, part, parts, lds, acc);
     share_put(acc, lds);
@@ -556,9 +547,8 @@ __global__ __launch_bounds__(64 * kShareTiles * kDenseParts) void moe_dense_down
     }
     __syncthreads();
   };
-  constexpr int kMost = 32 / kPieces, kHalf = 16 / kPieces;
-  for (int p0 = blockIdx.z * kMost; p0 < n; p0 += gridDim.z * kMost) {
-    if (n - p0 <= kHalf)
+  for (int p0 = blockIdx.z * kDensePairs; p0 < n; p0 += gridDim.z * kDensePairs) {
+    if (n - p0 <= 16 / kPieces)
       take(std::integral_constant<int, 4>{}, p0);
     else
       take(std::integral_constant<int, 8>{}, p0);
@@ -604,8 +594,8 @@ __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(const float* __res
 
 // From here on (two waves a SIMD) each wave takes a tile and all of its K;
 // with fewer tiles K is split over a workgroup's waves. 32 tokens, 128 experts
-// of 2048 x 768 (6144 and 8192 tiles): 41 + 26 us against 46 + 33; 7 tokens,
-// 10 experts of 1056 x 544 (340 tiles): 6.9 + 6.6 us against 5.3 + 5.3.
+// of 2048 x 768 (6144 and 8192 tiles): the call 73 us against 83; 7 tokens, 10
+// experts of 1056 x 544 (340 tiles): 6.9 + 6.6 us against 5.3 + 5.3.
 constexpr int64_t kManyTiles = 2048;
 
 // Rounds of `most` pairs that an expert with a quarter more than the average
@@ -636,15 +626,15 @@ hipError_t launch_tiles(Kernel kernel, int columns, int lds_per_wave, const Args
 
 // Whether every pair reads its expert's weights for itself. One token's
 // experts differ anyway, and several tokens seldom share one while there are
-// fewer pairs than experts (128 experts of 2048 x 768, top 8: 2 tokens 12.8 us
-// against 17.2 by experts, 8 tokens 31.6 against 34.6, 16 tokens 53.6 and 53.6,
-// 24 tokens 72.8 against 62.2). The less the pairs read, the better the caches
-// serve what they share, and the launch less counts: up to 1.5 pairs an expert
-// with 256 MiB (5 x 480 x 4640, 17 experts, top 3, 53 MB, 14.9 against 20.1; 8
-// x 4096 x 1440, 12 top 2, 150 MB, 26.0 and 25.9; 4 x 4096 x 14336, 8 top 2,
-// 749 MB, 124.8 against 109.4), up to four with 64 MiB (31 x 352 x 576, 76 top
-// 6, 60 MB, 15.5 against 18.3; 14 x 1792 x 576, 16 top 4, 92 MB, 19.4 against
-// 16.4).
+// fewer pairs than experts (128 experts of 2048 x 768, top 8: 2 tokens 12.4 us
+// against 23.3 by experts, 8 tokens 31.8 against 42.1, 16 tokens 53.2 against
+// 56.6, 24 tokens 73.7 against 67.1). The less the pairs read, the better the
+// caches serve what they share, and the launch less counts: up to 1.5 pairs an
+// expert with 256 MiB (5 x 480 x 4640, 17 experts, top 3, 53 MB, 14.9 against
+// 19.6; 22 x 2848 x 288, 125 top 7, 40.6 against 56.4; 8 x 4096 x 1440, 12 top
+// 2, 150 MB, 27.8 against 28.9; 4 x 4096 x 14336, 8 top 2, 749 MB, 127.6
+// against 117.4), up to four with 64 MiB (31 x 352 x 576, 76 top 6, 60 MB, 15.4
+// against 19.4; 14 x 1792 x 576, 16 top 4, 92 MB, 18.8 against 18.0).
 bool by_pairs(int T, int H, int I, int E, int top_k) {
   const int64_t pairs = (int64_t)T * top_k, bytes = pairs * 3 * H * I / 32 * 17;
   return T == 1 || pairs < E ||
@@ -688,22 +678,21 @@ hipError_t launch_pairs(const MoeArgs& m, hipStream_t stream) {
 hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   const int pairs = m.T * m.top_k, HB = m.H / 32, IB = m.I / 32, E = m.E;
   // Workspace: the pairs' parts of y, then the activations' pieces.
-  const int pieces = m.out_fp32 ? 3 : 2;
   float* part = m.workspace;
   auto* act = reinterpret_cast<uint16_t*>(part + (int64_t)pairs * m.H);
-  const UpArgs up = {m.x, m.ldx, m.w13, m.w13_s, act, HB, m.I, m.top_k, pieces};
+  const UpArgs up = {m.x, m.ldx, m.w13, m.w13_s, act, HB, m.I, m.top_k};
   const int64_t up_tiles = m.I / kFewTile, up_units = (HB + kUnitBlocks - 1) / kUnitBlocks;
   const bool up_waves = up_tiles * E >= kManyTiles;
   const auto launch_up = [&](auto kernel, int columns, int lds) {
     return launch_tiles(kernel, columns, lds, up, up_tiles, up_units, up_waves, m.ids, pairs, E,
                         stream);
   };
-  // Columns for up to 16 pairs in the first kernel, 8 in the second, cost
-  // registers, and waves, where most experts have few: from 4 and 2 pairs an
-  // expert on they pay (64 experts of 1024 x 1024, top 8, pairs an expert 2:
-  // 27.1 us with 8 and 8, 28.0 with 16 and 8, 29.3 with 8 and 4; 4: 35.5, 34.7
-  // and 37.8; 16: 70.3, 64.6 and 79.2; 64 experts of 4096 x 1024, 1.6: 83.1,
-  // 88.0 and 82.5).
+  // Columns for up to 16 pairs in the first kernel cost registers, and waves,
+  // where most experts have few: from 4 pairs an expert on they pay, or cost 3%
+  // (the call with 8 and with 16: 64 experts of 1024 x 1024, pairs an expert 2:
+  // 31.7 and 32.6 us, 4: 38.1 and 39.2, 6: 45.5 and 44.9, 16: 84.5 and 78.9;
+  // 64 of 4096 x 1024, 1.6: 88.1 and 96.3; 128 of 2048 x 768, 4: 93.5 and 89.9;
+  // 8 of 4096 x 14336, 4: 183 and 185, 6: 218 and 214).
   hipError_t e;
   if (pairs >= 4 * E)
     e = launch_up(up_waves ? moe_up_kernel<4, true> : moe_up_kernel<4, false>, 16,
@@ -716,36 +705,27 @@ hipError_t launch_experts(const MoeArgs& m, hipStream_t stream) {
   const int64_t down_tiles = m.H / (2 * kFewTile);
   const int64_t down_units = (IB + kUnitBlocks - 1) / kUnitBlocks;
   const bool down_waves = down_tiles * E >= kManyTiles;
-  const auto launch_down = [&](auto kernel, int columns, int lds) {
-    return launch_tiles(kernel, columns, lds, down, down_tiles, down_units, down_waves, m.ids,
-                        pairs, E, stream);
-  };
-  // Many pairs an expert and few tiles, but a workgroup a CU: 32 tokens through
-  // all 8 experts of 1024 x 1440 10.0 us against 16.5 (12.0 with its rounds in
-  // workgroups of their own), 64 tokens, 8 experts of 4096 x 14336, top 2 124
-  // against 154, 32 experts of 1024 x 1024, 8 pairs each, 11.8 against 13.5.
-  // Fewer pairs (12 experts of 4096 x 1440, 4 each: 17.5 against 15.2), fewer
-  // workgroups (192: 15.7 against 12.4) or many tiles (128 experts of 2048 x
-  // 768, 8 each: 69.8 against 45) do not pay.
-  const int most = 32 / pieces;
+  // Many pairs an expert and few tiles, but a workgroup a CU. The call with this
+  // kernel and without: 32 tokens, 4 experts of 2048 x 1536, top 4, 25.5 and
+  // 28.9 us; 64 tokens, 8 of 4096 x 14336, top 2, 333 and 383; 32 of 1024 x
+  // 1024, 8 pairs each, 28.6 and 31.3; 32 tokens through all 8 of 1024 x 1440
+  // 29.4 and 29.8. Fewer pairs (12 of 4096 x 1440, 4 each: 42.2 and 41.7) or
+  // many tiles (128 of 2048 x 768, 8 each: 143 and 121; 64 of 1024 x 1024, 16
+  // each: 84.6 and 78.8) do not pay.
   const int64_t blocks = (m.H + kShareTiles * kFewTile - 1) / (kShareTiles * kFewTile);
-  const int rounds = std::min(8, expected_rounds(pairs, E, most));
+  const int rounds = std::min(8, expected_rounds(pairs, E, kDensePairs));
   if (pairs >= 8 * E && !down_waves && blocks * E * rounds >= 256) {
     const int parts = IB > kUnitBlocks ? kDenseParts : 1;
     const int lds = std::max(share_lds_bytes<4>(parts), share_lds_bytes<8>(parts));
-    hipLaunchKernelGGL(m.out_fp32 ? moe_dense_down_kernel<3> : moe_dense_down_kernel<2>,
+    hipLaunchKernelGGL(moe_dense_down_kernel,
                        dim3(blocks, E, rounds), dim3(64 * kShareTiles * parts), lds, stream, down,
                        m.ids, pairs);
     e = hipGetLastError();
-  } else if (m.out_fp32)
-    e = launch_down(down_waves ? moe_down_kernel<4, 3, true> : moe_down_kernel<4, 3, false>, 4,
-                    few_lds_bytes<2, DownRows<4, 3>>());
-  else if (pairs >= 2 * E)
-    e = launch_down(down_waves ? moe_down_kernel<8, 2, true> : moe_down_kernel<8, 2, false>, 8,
-                    few_lds_bytes<2, DownRows<8, 2>>());
-  else
-    e = launch_down(down_waves ? moe_down_kernel<4, 2, true> : moe_down_kernel<4, 2, false>, 4,
-                    few_lds_bytes<2, DownRows<4, 2>>());
+  } else {
+    e = launch_tiles(down_waves ? moe_down_kernel<true> : moe_down_kernel<false>, kDownRows,
+                     few_lds_bytes<2, DownRows>(), down, down_tiles, down_units, down_waves, m.ids,
+                     pairs, E, stream);
+  }
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(m.out_fp32 ? moe_sum_kernel<true> : moe_sum_kernel<false>,
                      dim3((m.H / 2 + kSumThreads - 1) / kSumThreads, m.T), dim3(kSumThreads), 0,

@@ -548,7 +548,10 @@ def gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype=N
 
 # ------------------------------------------------ few-token tensor helpers
 # Called once per layer and token, where the host's time counts: their checks
-# and allocations are in the _tensors extension (csrc/tensors.cpp).
+# and allocations are in the _tensors extension (csrc/tensors.cpp). With
+# stream=s the call is ordered among s's work alone, its inputs have to be ready
+# there, and what it allocates is s's memory, which any stream that waits for s
+# may use.
 _ext = None
 
 

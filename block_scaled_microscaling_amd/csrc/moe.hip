@@ -6,8 +6,8 @@
 //   y[t, h] = sum_j weights[t, j] sum_i W2_e[h, i] a[p, i]
 // Weights are exact in BF16, sums and a are FP32. The second product takes a
 // as FP32 (by pairs) or as the sum of three BF16 pieces, all of FP32's
-// significand, in columns of the same MFMA, so that what a token gets does not
-// depend on which of the two the batch beside it takes. Two pieces, 16 bits,
+// significand, in columns of the same MFMA, so that a token's precision does
+// not depend on which of the two the batch beside it takes. Two pieces, 16 bits,
 // are 5 to 20% faster but change 0.2% of BF16 results by a step, and all that
 // is left of large activations that cancel. The first kernel by experts writes
 // the pieces, so that they are made once.

@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -99,11 +100,15 @@ struct Stream {
   void* handle;
   std::optional<c10::Stream> given;
 
-  // Memory that torch does not hand out again before a given stream (the
-  // current one's order torch keeps anyway) has used it.
+  // Memory of the call's stream: a block of another stream's may still be
+  // read or written by what that stream has queued. A given stream's output is
+  // meant for the current one, which torch waits for before it hands the
+  // memory out again.
   at::Tensor empty(at::IntArrayRef shape, const at::Tensor& like, at::ScalarType dtype) const {
+    if (!given) return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
+    const c10::StreamGuard guard(*given);
     at::Tensor t = at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
-    if (given) t.record_stream(*given);
+    if (guard.original_stream() != *given) t.record_stream(guard.original_stream());
     return t;
   }
 };

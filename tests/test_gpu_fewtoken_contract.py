@@ -37,3 +37,58 @@ def test_moe_bf16_result_is_the_fp32_result_rounded(T, H, I, E, k):
     got = run_moe(x, ids, w, ex, out_dtype=torch.bfloat16)
     differ = int((got != wide.bfloat16()).sum())
     assert differ == 0, f"{differ} of {got.numel()}"
+
+
+# ------------------------------------------------------------------ streams
+def side_calls(s):
+    """The three operators on inputs that are ready on s: name, call of a
+    stream (None: the current one) that returns a tuple."""
+    K, H, I, E, T = 512, 256, 96, 4, 24
+    with torch.cuda.stream(s):
+        x = bf16_to_dev(bf16_matrix((T, K), ("normal", 1.0, 0.0, 1.0), 1))
+        w = mx.quantize(bf16_to_dev(bf16_matrix((H, K), ("normal", 0.05, 0.0, 1.0), 2)))
+        h = bf16_to_dev(bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), 3))
+        router = bf16_to_dev(bf16_matrix((E, H), ("normal", 0.1, 0.0, 1.0), 4))
+        ids, p = choices(T, E, 2, 5)
+        ids, p = torch.from_numpy(ids).to(DEV), torch.from_numpy(p).to(DEV)
+        ex = tuple(u8_to_dev(a) for a in experts(E, H, I, 6))
+    torch.cuda.synchronize()
+    return [("gemv", lambda st: (mx.gemv(x, *w, stream=st),)),
+            ("moe_route", lambda st: mx.moe_route(h, router, 2, stream=st)),
+            ("moe", lambda st: (mx.moe(h, ids, p, *ex, stream=st),))]
+
+
+def test_outputs_on_a_given_stream_are_that_streams_memory():
+    """A block that the current stream has freed may still be used by what it
+    has queued: a call on another stream never gets it."""
+    announce("outputs on a given stream: whose memory")
+    s = torch.cuda.Stream()
+    for name, call in side_calls(s):
+        want = call(None)
+        torch.cuda.synchronize()
+        freed = [torch.empty_like(t) for t in want for _ in range(4)]
+        at = {t.data_ptr() for t in freed}
+        del freed
+        got = call(s)
+        torch.cuda.synchronize()
+        assert not at & {t.data_ptr() for t in got}, name
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_outputs_on_a_given_stream_beside_queued_work():
+    """The current stream still has writes of freed blocks queued when the call
+    on another stream is made and when it runs."""
+    announce("outputs on a given stream beside queued work")
+    s = torch.cuda.Stream()
+    for name, call in side_calls(s):
+        want = call(None)
+        torch.cuda.synchronize()
+        for i in range(6):
+            torch.cuda._sleep(1_000_000)
+            for t in want:
+                for _ in range(3):
+                    torch.empty_like(t).fill_(3)
+            got = call(s)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), f"{name}, round {i}"
+            del got

@@ -19,7 +19,9 @@ Two layers, same names as the C ABI:
     check their dtype, device, shape and contiguity, allocate outputs when none
     are given, enqueue on torch's current stream and raise Mxfp4Error on a
     non-zero status. gemv(...), moe_route(...) and moe(...) do the same for a
-    few BF16 rows against MXFP4 weights (a decode step).
+    few BF16 rows against MXFP4 weights (a decode step). With stream=s a call
+    is ordered among s's work alone: its inputs have to be ready there, what it
+    allocates is s's memory, and a stream that uses it has to wait for s.
 
 If the library is missing the functions raise: there is no fallback path.
 """
@@ -246,6 +248,20 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory of the call's stream: a block of another stream's may still be
+    read or written by what that stream has queued. The result of a given
+    stream is meant for the current one, so torch waits for that too before it
+    hands the memory out again."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _check(t, name, dtype, shape):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -271,9 +287,9 @@ def quantize(x, codes=None, scales=None, stream=None):
     M, K = x.shape
     _check(x, "x", torch.bfloat16, (M, K))
     if codes is None:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        codes = _empty((M, K // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+        scales = _empty((M, K // 32), torch.uint8, x.device, stream)
     _check(codes, "codes", torch.uint8, (M, K // 2))
     _check(scales, "scales", torch.uint8, (M, K // 32))
     rc = mxfp4_quantize_async(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(),
@@ -295,10 +311,10 @@ def quantize_2d(x, stream=None):
     M, K = x.shape
     _check(x, "x", torch.bfloat16, (M, K))
     dev = x.device
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
-    codes_t = torch.empty((K, M // 2), dtype=torch.uint8, device=dev)
-    scales_t = torch.empty((K, M // 32), dtype=torch.uint8, device=dev)
+    codes = _empty((M, K // 2), torch.uint8, dev, stream)
+    scales = _empty((M, K // 32), torch.uint8, dev, stream)
+    codes_t = _empty((K, M // 2), torch.uint8, dev, stream)
+    scales_t = _empty((K, M // 32), torch.uint8, dev, stream)
     rc = mxfp4_quantize_2d(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(),
                            codes_t.data_ptr(), scales_t.data_ptr(), _stream_handle(stream))
     if rc != 0:
@@ -327,9 +343,9 @@ def quantize_sr(x, seed, codes=None, scales=None, stream=None, row0=0):
     M, K = x.shape
     _check(x, "x", torch.bfloat16, (M, K))
     if codes is None:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        codes = _empty((M, K // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+        scales = _empty((M, K // 32), torch.uint8, x.device, stream)
     _check(codes, "codes", torch.uint8, (M, K // 2))
     _check(scales, "scales", torch.uint8, (M, K // 32))
     rc = mxfp4_quantize_sr_rows(x.data_ptr(), M, K, int(row0), _seed(seed), codes.data_ptr(),
@@ -353,10 +369,10 @@ def quantize_2d_sr(x, seed, stream=None, row0=0):
     M, K = x.shape
     _check(x, "x", torch.bfloat16, (M, K))
     dev = x.device
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
-    codes_t = torch.empty((K, M // 2), dtype=torch.uint8, device=dev)
-    scales_t = torch.empty((K, M // 32), dtype=torch.uint8, device=dev)
+    codes = _empty((M, K // 2), torch.uint8, dev, stream)
+    scales = _empty((M, K // 32), torch.uint8, dev, stream)
+    codes_t = _empty((K, M // 2), torch.uint8, dev, stream)
+    scales_t = _empty((K, M // 32), torch.uint8, dev, stream)
     rc = mxfp4_quantize_2d_sr_rows(x.data_ptr(), M, K, int(row0), _seed(seed), codes.data_ptr(),
                                    scales.data_ptr(), codes_t.data_ptr(), scales_t.data_ptr(),
                                    _stream_handle(stream))
@@ -395,7 +411,7 @@ def _gemm_call(fn, name, A_codes, A_scales, B_codes, B_scales, out_dtype, out, s
     _check(A_scales, "A_scales", torch.uint8, (M, K // 32))
     _check(B_scales, "B_scales", torch.uint8, (N, K // 32))
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A_codes.device)
+        out = _empty((M, N), out_dtype, A_codes.device, stream)
     _check(out, "out", out_dtype, (M, N))
     code = OUT_FP32 if out_dtype == torch.float32 else OUT_BF16
     rc = fn(A_codes.data_ptr(), A_scales.data_ptr(), B_codes.data_ptr(), B_scales.data_ptr(), M, N,
@@ -423,9 +439,9 @@ def gemm_swiglu(A_codes, A_scales, B_codes, B_scales, want_act=False, stream=Non
     _check(B_scales, "B_scales", torch.uint8, (N, K // 32))
     dev = A_codes.device
     Nh = N // 2
-    codes = torch.empty((M, Nh // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((M, max(Nh // 32, 0)), dtype=torch.uint8, device=dev)
-    act = torch.empty((M, Nh), dtype=torch.bfloat16, device=dev) if want_act else None
+    codes = _empty((M, Nh // 2), torch.uint8, dev, stream)
+    scales = _empty((M, max(Nh // 32, 0)), torch.uint8, dev, stream)
+    act = _empty((M, Nh), torch.bfloat16, dev, stream) if want_act else None
     rc = mxfp4_gemm_swiglu(A_codes.data_ptr(), A_scales.data_ptr(), B_codes.data_ptr(),
                            B_scales.data_ptr(), M, N, K, codes.data_ptr(), scales.data_ptr(),
                            None if act is None else act.data_ptr(), _stream_handle(stream))
@@ -446,8 +462,8 @@ def shuffle_b(B_codes, B_scales, stream=None):
     if rc != 0:
         raise Mxfp4Error(rc, "mxfp4_shuffle_b_sizes")
     dev = B_codes.device
-    codes_sh = torch.empty(cb, dtype=torch.uint8, device=dev)
-    scales_sh = torch.empty(sb, dtype=torch.uint8, device=dev)
+    codes_sh = _empty(cb, torch.uint8, dev, stream)
+    scales_sh = _empty(sb, torch.uint8, dev, stream)
     rc = mxfp4_shuffle_b(B_codes.data_ptr(), B_scales.data_ptr(), N, K, codes_sh.data_ptr(),
                          scales_sh.data_ptr(), _stream_handle(stream))
     if rc != 0:
@@ -472,7 +488,7 @@ def gemm_bshuffled(A_codes, A_scales, Bsh_codes, Bsh_scales, N, out_dtype=None, 
     _check(Bsh_codes, "Bsh_codes", torch.uint8, (cb,))
     _check(Bsh_scales, "Bsh_scales", torch.uint8, (sb,))
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A_codes.device)
+        out = _empty((M, N), out_dtype, A_codes.device, stream)
     _check(out, "out", out_dtype, (M, N))
     code = OUT_FP32 if out_dtype == torch.float32 else OUT_BF16
     rc = mxfp4_gemm_bshuffled(A_codes.data_ptr(), A_scales.data_ptr(), Bsh_codes.data_ptr(),
@@ -493,9 +509,9 @@ def quantize_frag(x, codes=None, scales=None, stream=None):
     M, K = x.shape
     _check(x, "x", torch.bfloat16, (M, K))
     if codes is None:
-        codes = torch.empty(M * K // 2, dtype=torch.uint8, device=x.device)
+        codes = _empty(M * K // 2, torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(M * K // 32, dtype=torch.uint8, device=x.device)
+        scales = _empty(M * K // 32, torch.uint8, x.device, stream)
     _check(codes, "codes", torch.uint8, (M * K // 2,))
     _check(scales, "scales", torch.uint8, (M * K // 32,))
     rc = mxfp4_quantize_frag(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(),
@@ -513,8 +529,8 @@ def to_frag(codes, scales, stream=None):
     K = 2 * Kh
     _check(codes, "codes", torch.uint8, (R, K // 2))
     _check(scales, "scales", torch.uint8, (R, K // 32))
-    cf = torch.empty(R * K // 2, dtype=torch.uint8, device=codes.device)
-    sf = torch.empty(R * K // 32, dtype=torch.uint8, device=codes.device)
+    cf = _empty(R * K // 2, torch.uint8, codes.device, stream)
+    sf = _empty(R * K // 32, torch.uint8, codes.device, stream)
     rc = mxfp4_to_frag(codes.data_ptr(), scales.data_ptr(), R, K, cf.data_ptr(), sf.data_ptr(),
                        _stream_handle(stream))
     if rc != 0:
@@ -535,7 +551,7 @@ def gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype=N
     _check(B_frag, "B_frag", torch.uint8, (N * K // 2,))
     _check(B_scales_frag, "B_scales_frag", torch.uint8, (N * K // 32,))
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A_frag.device)
+        out = _empty((M, N), out_dtype, A_frag.device, stream)
     _check(out, "out", out_dtype, (M, N))
     code = OUT_FP32 if out_dtype == torch.float32 else OUT_BF16
     rc = mxfp4_gemm_frag(A_frag.data_ptr(), A_scales_frag.data_ptr(), B_frag.data_ptr(),
@@ -548,10 +564,7 @@ def gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype=N
 
 # ------------------------------------------------ few-token tensor helpers
 # Called once per layer and token, where the host's time counts: their checks
-# and allocations are in the _tensors extension (csrc/tensors.cpp). With
-# stream=s the call is ordered among s's work alone, its inputs have to be ready
-# there, and what it allocates is s's memory, which any stream that waits for s
-# may use.
+# and allocations are in the _tensors extension (csrc/tensors.cpp).
 _ext = None
 
 

@@ -117,12 +117,13 @@ Stream stream_of(PyObject* o, c10::DeviceIndex device) {
   if (o == Py_None) return {c10::hip::getCurrentHIPStream(device).stream(), std::nullopt};
   TORCH_CHECK_TYPE(PyObject_IsInstance(o, reinterpret_cast<PyObject*>(THPStreamClass)) == 1,
                    "stream must be a torch.cuda.Stream");
+  const auto* s = reinterpret_cast<THPStream*>(o);
+  TORCH_CHECK_VALUE(s->device_index == device, "stream must be of the current device");
   PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
   if (!h) throw python_error();
   void* handle = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
   if (!handle && PyErr_Occurred()) throw python_error();
-  const auto* s = reinterpret_cast<THPStream*>(o);
   return {handle, c10::Stream::unpack3(s->stream_id, static_cast<c10::DeviceIndex>(s->device_index),
                                        static_cast<c10::DeviceType>(s->device_type))};
 }

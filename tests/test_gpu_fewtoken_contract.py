@@ -92,3 +92,13 @@ def test_outputs_on_a_given_stream_beside_queued_work():
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want)), f"{name}, round {i}"
             del got
+
+
+def test_stream_of_another_device_is_refused():
+    """Before its handle is asked for: no other device need be there."""
+    announce("stream of another device")
+    other = torch.cuda.Stream(stream_id=0, device_index=1, device_type=1)
+    assert other.device.index == 1
+    for name, call in side_calls(torch.cuda.Stream()):
+        with pytest.raises(ValueError, match="stream must be of the current device"):
+            call(other)

@@ -203,9 +203,12 @@ hipError_t launch_few(const uint8_t* x, int64_t ldx, const uint8_t* codes, const
                            (M + kFewTile - 1) / kFewTile);
   const auto kernel = out_fp32 ? gemv_few_kernel<T, XL, kAhead, true>
                                : gemv_few_kernel<T, XL, kAhead, false>;
-  if (kMaxWaves * few_lds_bytes<T, BfRows<XL>>() > 65536) {
+  // The limit is the process's, not the call's: every call sets the same one,
+  // so that none can lower it between another thread's set and launch.
+  constexpr int kMostLds = kMaxWaves * few_lds_bytes<T, BfRows<XL>>();
+  if (kMostLds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), lds, stream, x, ldx, codes, scales, M, N, KB,

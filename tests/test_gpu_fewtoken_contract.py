@@ -2,12 +2,14 @@
 type, the batch beside a token, streams, threads and addresses may not change
 it (GPU)."""
 
+import threading
+
 import pytest
 import torch
 
 from gpu_helpers import DEV, announce, bf16_to_dev, u8_to_dev
-from synth import bf16_matrix
-from test_gpu_fewtoken import choices, experts, run_moe
+from synth import bf16_matrix, random_codes, random_scales
+from test_gpu_fewtoken import N01, choices, experts, run_moe
 
 import block_scaled_microscaling_amd as mx
 
@@ -102,3 +104,38 @@ def test_stream_of_another_device_is_refused():
     for name, call in side_calls(torch.cuda.Stream()):
         with pytest.raises(ValueError, match="stream must be of the current device"):
             call(other)
+
+
+# ------------------------------------------------------------------ threads
+def test_calls_from_several_threads():
+    """Products whose kernel takes LDS by K, from threads of their own streams
+    at once: short K beside long ones."""
+    announce("gemv from four threads")
+    M, N = 16, 6200
+    cases = []
+    for i, K in enumerate((256, 8192, 1024, 4128)):
+        x = bf16_matrix((M, K), N01, i)
+        codes, scales = random_codes(N, K, i), random_scales(N, K, i)
+        cases.append((bf16_to_dev(x), u8_to_dev(codes), u8_to_dev(scales)))
+    want = [mx.gemv(*c, out_dtype=torch.float32) for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(50):
+                y = mx.gemv(*cases[i], out_dtype=torch.float32, stream=s)
+                s.synchronize()
+                if not torch.equal(y, want[i]):
+                    wrong.append(i)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001  (reported by the test's own thread)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong

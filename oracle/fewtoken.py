@@ -9,13 +9,15 @@ how far an FP32 evaluation of the same sums may be from it:
     additions of one matrix instruction, one per following instruction (K /
     32) and those of the partial sums' reduction (at most 32), each at most
     half a unit in the last place of a partial sum, which S = sum |products|
-    bounds: |y - y_exact| <= (K / 32 + 64) 2^-24 S;
+    bounds: |y - y_exact| <= (K / 32 + 64) 2^-24 S; and where only n products
+    are not zero only n additions round, so n in place of K / 32 + 64 if less;
   * silu(g) u from inexact g, u: |silu'| <= 1.1, so |a - a_exact| <= 1.1 dg
     (|u| + du) + |silu(g)| du + eval, where eval covers the FP32 evaluation
     (rounded exponent argument, exp, add, divide, product): (2 |g| + 16)
     2^-24 |a|, and |a| itself where exp(-g) passes FP32's range (g < -87);
-  * the activation carried as two BF16 values: each rounding is off by at
-    most 2^-8 of what it rounds, so the pair by 2^-16 |a|.
+  * the activation is FP32 between the two products, also where three BF16
+    values hold it (3 x 8 bits of significand): then it is three sums, of
+    which the two of the rests hardly count, and the two additions of them.
 """
 
 import numpy as np
@@ -26,15 +28,18 @@ U = 2.0 ** -24
 TINY = 2.0 ** -126      # products below FP32's normal range may count as zero
 
 
-def _sum_tol(K, S):
-    return (K / 32 + 64) * U * S + K * TINY
+def _sum_tol(K, x, w, pieces=1):
+    """How far an FP32 x @ w^T over K may be off, x of so many pieces."""
+    x, w = np.abs(x), np.abs(w).T
+    S, n = x @ w, (x > 0).astype(np.float64) @ (w > 0)
+    return np.minimum(K / 32 + 63 + pieces, pieces * n) * U * S + pieces * K * TINY
 
 
 def gemv(x_bits, codes, scales):
     """(y, tol) float64 [M, N]: y = x dq(W)^T and the FP32 tolerance."""
     x = bf16_bits_to_f64(np.asarray(x_bits, dtype=np.uint16))
     w = dequantize(codes, scales)
-    return x @ w.T, _sum_tol(x.shape[1], np.abs(x) @ np.abs(w).T)
+    return x @ w.T, _sum_tol(x.shape[1], x, w)
 
 
 def route(x_bits, router_bits, top_k, renormalize):
@@ -78,16 +83,15 @@ def moe(x_bits, ids, weights, w13_codes, w13_scales, w2_codes, w2_scales):
         w13 = dequantize(w13_codes[e], w13_scales[e])
         w2 = dequantize(w2_codes[e], w2_scales[e])
         gu = x[t] @ w13.T
-        dgu = _sum_tol(H, np.abs(x[t]) @ np.abs(w13).T)
+        dgu = _sum_tol(H, x[t], w13)
         g, u, dg, du = gu[:, :I], gu[:, I:], dgu[:, :I], dgu[:, I:]
         with np.errstate(over="ignore"):
             silu = g / (1.0 + np.exp(-g))
         a = silu * u
         da = 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du
         da += (2 * np.abs(g) + 16) * U * np.abs(a) + np.where(g < -87, np.abs(a), 0.0)
-        da += 2.0 ** -16 * (np.abs(a) + da)
         part = a @ w2.T
-        dpart = da @ np.abs(w2).T + _sum_tol(2 * I, (np.abs(a) + da) @ np.abs(w2).T)
+        dpart = da @ np.abs(w2).T + _sum_tol(I, np.abs(a) + da, w2, pieces=3)
         wj = weights[t, j][:, None]
         np.add.at(y, t, wj * part)
         np.add.at(tol, t, np.abs(wj) * dpart)

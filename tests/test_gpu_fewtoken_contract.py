@@ -7,9 +7,11 @@ import threading
 import pytest
 import torch
 
+from fewtoken_cases import one_product_experts
 from gpu_helpers import DEV, announce, bf16_to_dev, u8_to_dev
+from oracle import fewtoken
 from synth import bf16_matrix, random_codes, random_scales
-from test_gpu_fewtoken import N01, choices, experts, run_moe
+from test_gpu_fewtoken import N01, check, choices, experts, run_moe
 
 import block_scaled_microscaling_amd as mx
 
@@ -39,6 +41,16 @@ def test_moe_bf16_result_is_the_fp32_result_rounded(T, H, I, E, k):
     got = run_moe(x, ids, w, ex, out_dtype=torch.bfloat16)
     differ = int((got != wide.bfloat16()).sum())
     assert differ == 0, f"{differ} of {got.numel()}"
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,H,I,E,k", BY_PAIRS + BY_EXPERTS)
+def test_moe_activation_to_its_last_bit(T, H, I, E, k, out):
+    """Sums of one product each, so that the tolerance is a few roundings and
+    a lost third part of an activation would show in FP32 results."""
+    announce(f"moe of single products, T{T} H{H} I{I} E{E} k{k} {out}")
+    x, ids, w, ex = one_product_experts(T, H, I, E, k, T + I)
+    check(run_moe(x, ids, w, ex, out_dtype=out), *fewtoken.moe(x, ids, w, *ex))
 
 
 # ------------------------------------------------------------------ streams

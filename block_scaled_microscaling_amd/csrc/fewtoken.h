@@ -299,10 +299,12 @@ __device__ __forceinline__ void few_stream(const uint8_t* const (&codes)[T],
   }
 }
 
-// The next BF16 piece of v, which becomes its rest: FP32 holds it exactly, at
-// most 2^-8 of the value.
+// The next BF16 piece of v, which becomes its rest: the first 8 bits of the
+// significand, the rest being exact, so three pieces are all 24. Cut and not
+// rounded: FP32 values next to the largest would round to infinity. (Bits below
+// BF16's least, 2^-133, are lost: of values under 2^-109.)
 __device__ __forceinline__ uint16_t next_piece(float& v) {
-  const uint32_t bits = pack_bf16x2(v, v) << 16;
+  const uint32_t bits = __float_as_uint(v) & 0xFFFF0000u;
   // No rest where the piece is no finite number: inf - inf is NaN.
   v = (bits & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(bits);
   return (uint16_t)(bits >> 16);

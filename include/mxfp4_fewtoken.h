@@ -65,7 +65,8 @@ int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, in
 /* The experts of an MoE layer for T routed tokens:
  *   y[t] = sum_j weights[t, j] * W2_e (silu(Wg_e x[t]) * (Wu_e x[t])),
  *   e = ids[t, j], silu(z) = z / (1 + exp(-z)), in FP32 up to y, whatever
- *   its type and however many tokens there are.
+ *   its type and however many tokens there are (several tokens' activations
+ *   may lose bits below 2^-133).
  * An id outside 0 .. E - 1 adds nothing and its weight is not read into the
  * sum (an expert that another device holds); a token with no expert here
  * gets zeros. A token may name an expert more than once.

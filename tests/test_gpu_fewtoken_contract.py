@@ -4,13 +4,14 @@ it (GPU)."""
 
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 from fewtoken_cases import one_product_experts
 from gpu_helpers import DEV, announce, bf16_to_dev, u8_to_dev
 from oracle import fewtoken
-from synth import bf16_matrix, random_codes, random_scales
+from synth import bf16_matrix, f32_to_bf16_bits, random_codes, random_scales
 from test_gpu_fewtoken import N01, check, choices, experts, run_moe
 
 import block_scaled_microscaling_amd as mx
@@ -51,6 +52,28 @@ def test_moe_activation_to_its_last_bit(T, H, I, E, k, out):
     announce(f"moe of single products, T{T} H{H} I{I} E{E} k{k} {out}")
     x, ids, w, ex = one_product_experts(T, H, I, E, k, T + I)
     check(run_moe(x, ids, w, ex, out_dtype=out), *fewtoken.moe(x, ids, w, *ex))
+
+
+@pytest.mark.parametrize("T,H,I,E,k", BY_PAIRS + BY_EXPERTS)
+def test_moe_activation_next_to_fp32s_largest(T, H, I, E, k):
+    """g = u = 2^64 (1 - 2^-12) exactly, so a = 2^128 (1 - 2^-11 + 2^-24) is
+    finite in FP32 and above BF16's largest value; W2 takes 2^-11 of it."""
+    announce(f"moe of the largest activations, T{T} H{H} I{I} E{E} k{k}")
+    x = np.zeros((T, H), np.float32)
+    x[:, 0], x[:, 1] = 2.0 ** 64 * (255 / 256), 15 * 2.0 ** 52
+    c1 = np.zeros((E, 2 * I, H // 2), np.uint8)
+    c1[:, :, 0] = 0x22                         # 1.0 and 1.0
+    c2 = np.zeros((E, H, I // 2), np.uint8)
+    c2[:, :, 0] = 0x01                         # 0.5
+    ex = (c1, np.full((E, 2 * I, H // 32), 127, np.uint8), c2,
+          np.full((E, H, I // 32), 117, np.uint8))
+    ids = np.full((T, k), -1, np.int32)
+    ids[:, 0] = np.arange(T) % E
+    want = 2.0 ** 117 * (1 - 2.0 ** -11 + 2.0 ** -24)
+    for out in (torch.float32, torch.bfloat16):
+        got = run_moe(f32_to_bf16_bits(x), ids, np.ones((T, k), np.float32), ex, out_dtype=out)
+        exact = torch.full((T, H), want, dtype=torch.float64).to(out).to(DEV)
+        assert torch.equal(got, exact), got.flatten()[:4].tolist()
 
 
 # ------------------------------------------------------------------ streams

@@ -586,8 +586,9 @@ __global__ __launch_bounds__(kSumThreads) void moe_sum_kernel(const float* __res
       }
     }
   }
+  const float sum[2] = {s0, s1};  // y is 4-byte aligned and no more
   if constexpr (kOutFp32)
-    *reinterpret_cast<float2*>(static_cast<float*>(y) + t * H + h) = make_float2(s0, s1);
+    __builtin_memcpy(static_cast<float*>(y) + t * H + h, &sum, 8);
   else
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(y) + t * H + h) = pack_bf16x2(s0, s1);
 }

@@ -174,3 +174,42 @@ def test_calls_from_several_threads():
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+# ---------------------------------------------------------------- addresses
+@pytest.mark.parametrize("T,H,I,E,k", BY_PAIRS + BY_EXPERTS)
+def test_moe_result_at_any_four_byte_address(T, H, I, E, k):
+    """y, ids and weights one element past a 16-byte boundary, nothing around y
+    written."""
+    announce(f"moe at 4-byte addresses, T{T} H{H} I{I} E{E} k{k}")
+    x = bf16_matrix((T, H), ("normal", 1.0, 0.0, 1.0), T + H)
+    ids, w = choices(T, E, k, I, 0.1)
+    ex = tuple(u8_to_dev(a) for a in experts(E, H, I, E + k))
+    def off(a):
+        return torch.cat([torch.zeros(1, dtype=a.dtype), a.flatten()]).to(DEV)[1:].view(a.shape)
+
+    ids, w = torch.from_numpy(ids), torch.from_numpy(w)
+    want = mx.moe(bf16_to_dev(x), ids.to(DEV), w.to(DEV), *ex, out_dtype=torch.float32)
+    for dt, lead in ((torch.float32, 1), (torch.bfloat16, 2)):
+        buf = torch.full((T * H + 2 * lead,), 7.0, dtype=dt, device=DEV)
+        out = buf[lead:-lead].view(T, H)
+        assert out.data_ptr() % 16 == 4
+        mx.moe(bf16_to_dev(x), off(ids), off(w), *ex, out=out)
+        assert torch.equal(out, want.to(dt))
+        assert torch.all(buf[:lead] == 7.0) and torch.all(buf[-lead:] == 7.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 333, 512), (1, 333, 4128), (3, 333, 512), (16, 333, 512),
+                                   (16, 6200, 512), (16, 14337, 512)])
+def test_gemv_result_at_any_four_byte_address(M, N, K):
+    announce(f"gemv at 4-byte addresses, {M} x {N} x {K}")
+    x = bf16_to_dev(bf16_matrix((M, K), N01, M))
+    w = u8_to_dev(random_codes(N, K, N)), u8_to_dev(random_scales(N, K, K))
+    for dt, lead in ((torch.float32, 1), (torch.bfloat16, 2)):
+        want = mx.gemv(x, *w, out_dtype=dt)
+        buf = torch.full((M * N + 2 * lead,), 7.0, dtype=dt, device=DEV)
+        out = buf[lead:-lead].view(M, N)
+        assert out.data_ptr() % 16 == 4
+        mx.gemv(x, *w, out=out)
+        assert torch.equal(out, want)
+        assert torch.all(buf[:lead] == 7.0) and torch.all(buf[-lead:] == 7.0)

@@ -19,7 +19,6 @@ constexpr int64_t kMaxMoeDim = int64_t(1) << 20;
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopK = 32;
 constexpr int64_t kMaxRouteT = 65535;
-constexpr int64_t kMaxPairs = 1024;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -91,7 +90,8 @@ int mxfp4_moe_route(const void* x_bf16, int64_t ldx, const void* router_bf16, in
 }
 
 int mxfp4_moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top_k, int64_t* bytes) {
-  if (!bytes || T < 1 || top_k < 1 || top_k > kMaxTopK || T > kMaxPairs || T * top_k > kMaxPairs)
+  if (!bytes || T < 1 || top_k < 1 || top_k > kMaxTopK || T > mxfp4::kMaxPairs ||
+      T * top_k > mxfp4::kMaxPairs)
     return MXFP4_EINVAL;
   if (H < 32 || H % 32 != 0 || H > kMaxMoeDim || I < 32 || I % 32 != 0 || I > kMaxMoeDim)
     return MXFP4_EINVAL;

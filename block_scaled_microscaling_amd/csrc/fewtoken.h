@@ -19,7 +19,9 @@ namespace mxfp4 {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
-constexpr int kFewTile = 16;  // weight rows and activation rows of one MFMA
+constexpr int kFewTile = 16;     // weight rows and activation rows of one MFMA
+constexpr int kMaxWaves = 8;     // of a workgroup whose waves are segments of K
+constexpr int kMaxPairs = 1024;  // T top_k of moe: its kernels' list of pairs is in LDS
 
 __device__ __forceinline__ float scale_of_byte(uint32_t byte) {
   return __uint_as_float(byte << 23);
@@ -33,6 +35,14 @@ __device__ __forceinline__ bf16x8_t decode8(uint32_t w, float scale) {
   const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
   const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
   return (bf16x8_t){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <bool kOutFp32>
+__device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
+  if constexpr (kOutFp32)
+    static_cast<float*>(y)[at] = v;
+  else
+    static_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16x2(v, v);
 }
 
 // Orders the LDS accesses of one wave's lanes among each other.

@@ -16,8 +16,6 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kMaxWaves = 8;
-
 // Workgroups along N: a grid's extent counts threads in 32 bits, so rows of
 // kGridX workgroups are stacked along z.
 constexpr int64_t kGridX = 1 << 20;
@@ -29,14 +27,6 @@ __device__ __forceinline__ int64_t block_n() {
 dim3 grid_n(int64_t blocks, int y) {
   return blocks <= kGridX ? dim3((uint32_t)blocks, y)
                           : dim3((uint32_t)kGridX, y, (uint32_t)((blocks + kGridX - 1) / kGridX));
-}
-
-template <bool kOutFp32>
-__device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
-  if constexpr (kOutFp32)
-    static_cast<float*>(y)[at] = v;
-  else
-    static_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16x2(v, v);
 }
 
 // One row of x. A wave takes 64 blocks (2048 k) of four weight rows, a block

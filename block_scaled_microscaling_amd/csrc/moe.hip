@@ -33,22 +33,12 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kMaxWaves = 8;
 constexpr int kPairDownRows = 8;
 constexpr int kPairDownWaves = 7;  // 63 KiB of LDS
-constexpr int kMaxPairs = 1024;
 constexpr int kTileWaves = 4;   // of the kernels for several tokens
 constexpr int kDenseParts = 2;  // parts of K of the kernel for many pairs an expert
 constexpr int kPieces = 3;      // BF16 pieces of an activation
 constexpr int kDownRows = 4;    // pairs of the second kernel by experts: 12 columns
-
-template <bool kOutFp32>
-__device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
-  if constexpr (kOutFp32)
-    static_cast<float*>(y)[at] = v;
-  else
-    static_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16x2(v, v);
-}
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 

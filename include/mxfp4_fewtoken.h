@@ -48,7 +48,7 @@ int mxfp4_gemv(const void* x_bf16, int64_t ldx, const void* W_codes, const void*
  *   ids[j]     = the expert with the (j + 1)-th largest l, j < top_k; of
  *                equal ones the lowest index first
  *   weights[j] = p[ids[j]], divided by the sum of the top_k chosen ones when
- *                renormalize is 1
+ *                renormalize is 1; in 64 bits, rounded to FP32 once
  * x_bf16 [T, H] as mxfp4_gemv's x; router_bf16 [E, H] BF16, 16-byte aligned
  * ids [T, top_k] int32, weights [T, top_k] FP32: 4-byte aligned
  * workspace: mxfp4_moe_route_workspace bytes, 16-byte aligned, any content;

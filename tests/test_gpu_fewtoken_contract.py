@@ -213,3 +213,23 @@ def test_gemv_result_at_any_four_byte_address(M, N, K):
         mx.gemv(x, *w, out=out)
         assert torch.equal(out, want)
         assert torch.all(buf[:lead] == 7.0) and torch.all(buf[-lead:] == 7.0)
+
+
+# ------------------------------------------------------------------- router
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,H,E,k,spread", [
+    (1, 4096, 8, 2, 1.0), (7, 296, 120, 8, 1.0), (13, 2856, 61, 4, 1.0), (64, 4096, 128, 8, 1.0),
+    (5, 1024, 256, 8, 1.0), (3, 256, 1000, 32, 1.0),
+    (9, 512, 48, 32, 12.0), (9, 512, 300, 32, 12.0),   # weights down to 2^-100
+])
+def test_route_weights_are_rounded_once(T, H, E, k, spread, renorm):
+    """64-bit logits, exponentials and sums: a weight is FP32's nearest, or next
+    to it where 64 bits are at a border (H 2^-53 of a logit's products)."""
+    announce(f"route weights {T} x {H}, {E} top {k}, spread {spread}, renorm {renorm}")
+    x = bf16_matrix((T, H), ("normal", spread, 0.0, 1.0), T)
+    r = bf16_matrix((E, H), ("normal", 1.0 / np.sqrt(H), 0.0, 1.0), E)
+    ids, w = mx.moe_route(bf16_to_dev(x), bf16_to_dev(r), k, renormalize=renorm)
+    want_ids, want, _ = fewtoken.route(x, r, k, renorm)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    off = np.abs(w.double().cpu().numpy() - want) / np.maximum(want, 2.0 ** -126)
+    assert off.max() <= 2.0 ** -24 * (1 + 2.0 ** -10), off.max() * 2.0 ** 24

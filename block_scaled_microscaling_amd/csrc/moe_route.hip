@@ -9,8 +9,8 @@
 // off by 2 to 3 times as much, and by 2^-24 of a far logit's distance.
 //
 // What bounds it: a few tokens' launches and latencies (1 token x 4096, 8
-// experts 3.6 us; 64 tokens x 4096, 128 experts 5.1 + 4.2), many tokens' 2 T E
-// H flop of 64-bit arithmetic (512 tokens x 4096, 128 experts 20 us). The
+// experts 3.7 us; 64 tokens x 4096, 128 experts 5.0 + 4.2), many tokens' 2 T E
+// H flop of 64-bit arithmetic (512 tokens x 4096, 128 experts 21 us). The
 // bytes are few.
 //
 // Few experts: one workgroup a token does it all (one launch). Otherwise the

@@ -146,3 +146,33 @@ def test_gemv_of_more_workgroups_than_a_grids_row(M, N, K, rows):
     want, tol = fewtoken.gemv(x.view(torch.int16).cpu().numpy().view(np.uint16),
                               codes[at].cpu().numpy(), scales[at].cpu().numpy())
     check(got[:, at], want, tol)
+
+
+def test_layer_captured_on_a_forked_stream():
+    """Calls of a given stream inside a capture, joined before its end; what
+    they allocate belongs to the graph."""
+    announce("layer captured on a forked stream")
+    T, K, H, I, E, k = LAYERS[0]
+    layer = Layer(K, H, I, E, k, 41)
+    inputs = inputs_of(T, K, 3)
+    x = inputs[0].clone()
+    s = torch.cuda.Stream()
+    layer(x, stream=s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = layer(x, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    for i, inp in enumerate(inputs):
+        x.copy_(inp)
+        want = layer(x)
+        torch.cuda.synchronize()
+        for _ in range(2):
+            for t in got:
+                t.fill_(77)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert equal(got, want), f"replay {i}"
+            _ = (inp.float() * 2).sum().item()

@@ -1,7 +1,8 @@
-"""MXFP4 quantize and block-scaled GEMM on AMD gfx950 (MI355X).
+"""MXFP4 and FP8 quantize and block-scaled GEMM on AMD gfx950 (MI355X).
 
-A thin binding over the C ABI of libmxfp4.so (include/mxfp4.h and, for the
-few-token operators, include/mxfp4_fewtoken.h). Every step
+A thin binding over the C ABI of libmxfp4.so (include/mxfp4.h, for the
+few-token operators include/mxfp4_fewtoken.h, for the FP8 operators
+include/mxfp4_fp8.h). Every step
 of the computation runs in the library's HIP kernels; this module only
 marshals arguments. PyTorch supplies device memory and streams.
 
@@ -11,15 +12,20 @@ Two layers, same names as the C ABI:
     mxfp4_quantize_sr_rows, mxfp4_quantize_2d_sr_rows, mxfp4_gemm,
     mxfp4_gemm_tile, mxfp4_gemm_swiglu, mxfp4_shuffle_b(_sizes), mxfp4_gemm_bshuffled,
     mxfp4_quantize_frag, mxfp4_to_frag, mxfp4_gemm_frag, mxfp4_gemv,
-    mxfp4_moe_route(_workspace), mxfp4_moe(_workspace) take raw device
-    pointers (ints) and return the C status code.
+    mxfp4_moe_route(_workspace), mxfp4_moe(_workspace),
+    mxfp4_quantize_fp8(_2d), mxfp4_gemm_fp8, mxfp4_gemm_fp8_swiglu(_workspace),
+    mxfp4_swiglu_fp8_backward take raw device pointers (ints) and return the
+    C status code.
   * quantize(x), quantize_2d(x), quantize_sr(x, seed, row0=0),
     quantize_2d_sr(x, seed, row0=0), gemm(...), gemm_tile(...) and
     gemm_swiglu(...) take torch tensors,
     check their dtype, device, shape and contiguity, allocate outputs when none
     are given, enqueue on torch's current stream and raise Mxfp4Error on a
     non-zero status. gemv(...), moe_route(...) and moe(...) do the same for a
-    few BF16 rows against MXFP4 weights (a decode step). With stream=s a call
+    few BF16 rows against MXFP4 weights (a decode step), and quantize_fp8(x),
+    quantize_fp8_2d(x), gemm_fp8(...), gemm_fp8_swiglu(...) and
+    swiglu_fp8_backward(...) for FP8 operands with a scale for each block of
+    128. With stream=s a call
     is ordered among s's work alone: its inputs have to be ready there, what it
     allocates is s's memory, and a stream that uses it has to wait for s.
 
@@ -41,10 +47,19 @@ __all__ = [
     "quantize_frag", "to_frag", "gemm_frag",
     "mxfp4_gemv", "mxfp4_moe_route_workspace", "mxfp4_moe_route", "mxfp4_moe_workspace",
     "mxfp4_moe", "gemv", "moe_route_workspace", "moe_route", "moe_workspace", "moe",
+    "FP8_E4M3", "FP8_E5M2", "SCALE_UE8M0", "SCALE_FP32",
+    "mxfp4_quantize_fp8", "mxfp4_quantize_fp8_2d", "mxfp4_gemm_fp8",
+    "mxfp4_gemm_fp8_swiglu_workspace", "mxfp4_gemm_fp8_swiglu", "mxfp4_swiglu_fp8_backward",
+    "quantize_fp8", "quantize_fp8_2d", "gemm_fp8", "gemm_fp8_swiglu_workspace",
+    "gemm_fp8_swiglu", "swiglu_fp8_backward",
 ]
 
 OUT_BF16 = 0
 OUT_FP32 = 1
+FP8_E4M3 = 0
+FP8_E5M2 = 1
+SCALE_UE8M0 = 0
+SCALE_FP32 = 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libmxfp4.so")
@@ -115,6 +130,20 @@ def load_library():
         lib.mxfp4_moe.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32,
                                   vp, vp, vp]
         lib.mxfp4_moe.restype = i32
+        lib.mxfp4_quantize_fp8.argtypes = [vp, i64, i64, i64, i64, i32, i32, vp, vp, vp]
+        lib.mxfp4_quantize_fp8.restype = i32
+        lib.mxfp4_quantize_fp8_2d.argtypes = [vp, i64, i64, i64, i64, i32, i32, vp, vp, vp, vp,
+                                              vp]
+        lib.mxfp4_quantize_fp8_2d.restype = i32
+        lib.mxfp4_gemm_fp8.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, i32, vp, vp]
+        lib.mxfp4_gemm_fp8.restype = i32
+        lib.mxfp4_gemm_fp8_swiglu_workspace.argtypes = [i64, i64, i64, pi64]
+        lib.mxfp4_gemm_fp8_swiglu_workspace.restype = i32
+        lib.mxfp4_gemm_fp8_swiglu.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp,
+                                              vp]
+        lib.mxfp4_gemm_fp8_swiglu.restype = i32
+        lib.mxfp4_swiglu_fp8_backward.argtypes = [vp, vp, i64, i64, i32, vp, vp, vp, vp, vp]
+        lib.mxfp4_swiglu_fp8_backward.restype = i32
         _lib = lib
     return _lib
 
@@ -239,6 +268,47 @@ def mxfp4_moe(x_bf16, ldx, ids, weights, W13_codes, W13_scales, W2_codes, W2_sca
     return int(load_library().mxfp4_moe(x_bf16, ldx, ids, weights, W13_codes, W13_scales,
                                         W2_codes, W2_scales, T, H, I, E, top_k, out_dtype, y,
                                         workspace, stream))
+
+
+def mxfp4_quantize_fp8(x_bf16, ldx, M, K, block_rows, code_type, scale_type, codes, scales,
+                       stream):
+    return int(load_library().mxfp4_quantize_fp8(x_bf16, ldx, M, K, block_rows, code_type,
+                                                 scale_type, codes, scales, stream))
+
+
+def mxfp4_quantize_fp8_2d(x_bf16, ldx, M, K, block_rows, code_type, scale_type, codes, scales,
+                          codes_t, scales_t, stream):
+    return int(load_library().mxfp4_quantize_fp8_2d(x_bf16, ldx, M, K, block_rows, code_type,
+                                                    scale_type, codes, scales, codes_t, scales_t,
+                                                    stream))
+
+
+def mxfp4_gemm_fp8(A_codes, A_type, A_scales, B_codes, B_scales, scale_type, B_block_rows, M, N,
+                   K, out_dtype, C, stream):
+    return int(load_library().mxfp4_gemm_fp8(A_codes, A_type, A_scales, B_codes, B_scales,
+                                             scale_type, B_block_rows, M, N, K, out_dtype, C,
+                                             stream))
+
+
+def mxfp4_gemm_fp8_swiglu_workspace(M, I, K):
+    """(rc, bytes) of gemm_fp8_swiglu's workspace."""
+    n = ctypes.c_int64(0)
+    rc = int(load_library().mxfp4_gemm_fp8_swiglu_workspace(M, I, K, ctypes.byref(n)))
+    return rc, n.value
+
+
+def mxfp4_gemm_fp8_swiglu(A_codes, A_scales, W13_codes, W13_scales, M, I, K, codes, scales,
+                          act_bf16, gu_bf16, workspace, stream):
+    return int(load_library().mxfp4_gemm_fp8_swiglu(A_codes, A_scales, W13_codes, W13_scales, M,
+                                                    I, K, codes, scales, act_bf16, gu_bf16,
+                                                    workspace, stream))
+
+
+def mxfp4_swiglu_fp8_backward(dact_bf16, gu_bf16, M, I, code_type, codes, scales, codes_t,
+                              scales_t, stream):
+    return int(load_library().mxfp4_swiglu_fp8_backward(dact_bf16, gu_bf16, M, I, code_type,
+                                                        codes, scales, codes_t, scales_t,
+                                                        stream))
 
 
 # ------------------------------------------------------- torch tensor layer
@@ -562,7 +632,7 @@ def gemm_frag(A_frag, A_scales_frag, B_frag, B_scales_frag, M, N, K, out_dtype=N
     return out
 
 
-# ------------------------------------------------ few-token tensor helpers
+# ---------------------------------------- few-token and FP8 tensor helpers
 # Called once per layer and token, where the host's time counts: their checks
 # and allocations are in the _tensors extension (csrc/tensors.cpp).
 _ext = None
@@ -649,3 +719,95 @@ def moe(x, ids, weights, w13_codes, w13_scales, w2_codes, w2_scales, out_dtype=N
     if type(y) is int:
         raise Mxfp4Error(y, "mxfp4_moe")
     return y
+
+
+def quantize_fp8(x, block_rows=1, dtype=None, scale_dtype=None, codes=None, scales=None,
+                 stream=None):
+    """BF16 -> FP8 with a power-of-two scale for each block of 128 elements of
+    a row (block_rows=1: activations) or each 128 x 128 block (block_rows=128:
+    weights). x: bfloat16 [M, K] (rows contiguous, row stride a multiple of
+    8), K % 16 == 0.
+
+    dtype: torch.float8_e4m3fn (default) or torch.float8_e5m2. scale_dtype:
+    torch.uint8 (default; UE8M0 bytes) or torch.float32. Returns (codes [M, K],
+    scales [M, ceil(K/128)] or [ceil(M/128), ceil(K/128)]).
+    """
+    r = (_ext or load_tensors()).quantize_fp8(x, block_rows, dtype, scale_dtype, codes, scales,
+                                              stream)
+    if type(r) is int:
+        raise Mxfp4Error(r, "mxfp4_quantize_fp8")
+    return r
+
+
+def quantize_fp8_2d(x, block_rows=1, dtype=None, scale_dtype=None, stream=None):
+    """quantize_fp8 of x and of x^T in one pass: the operands of a product and
+    of its gradients.
+
+    Returns (codes, scales, codes_t [K, Mp], scales_t): the forms of x and of
+    x^T, the latter's rows filled with zeros from M to Mp, M rounded up to a
+    multiple of 16.
+    """
+    r = (_ext or load_tensors()).quantize_fp8_2d(x, block_rows, dtype, scale_dtype, stream)
+    if type(r) is int:
+        raise Mxfp4Error(r, "mxfp4_quantize_fp8_2d")
+    return r
+
+
+def gemm_fp8(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=None):
+    """C[M, N] = dq(a) @ dq(b)^T from FP8 operands: a [M, K] (float8_e4m3fn or
+    float8_e5m2) with scales [M, ceil(K/128)], b [N, K] (float8_e4m3fn) with
+    scales [ceil(N/128), ceil(K/128)] (a weight's 128 x 128 blocks) or, UE8M0
+    only, [N, ceil(K/128)]. Scales are uint8 (UE8M0) or float32, both alike;
+    any M and N, K % 16 == 0.
+
+    out_dtype: torch.bfloat16 (default) or torch.float32.
+    """
+    y = (_ext or load_tensors()).gemm_fp8(a, a_scales, b, b_scales, out_dtype, out, stream)
+    if type(y) is int:
+        raise Mxfp4Error(y, "mxfp4_gemm_fp8")
+    return y
+
+
+def gemm_fp8_swiglu_workspace(M, I, K):
+    """A workspace for gemm_fp8_swiglu on M rows of K, width I (uint8)."""
+    import torch
+    rc, nbytes = mxfp4_gemm_fp8_swiglu_workspace(M, I, K)
+    if rc != 0:
+        raise Mxfp4Error(rc, "mxfp4_gemm_fp8_swiglu_workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def gemm_fp8_swiglu(a, a_scales, w13, w13_scales, want_act=False, want_gu=False, workspace=None,
+                    stream=None):
+    """Gate+up product of a gated MLP on FP8 operands, its activation
+    act = silu(g) * u quantized for the down product.
+
+    a [M, K] with scales [M, ceil(K/128)]; w13 [2I, K] the stacked
+    [W_gate; W_up] with scales of 128 x 128 blocks [2I/128, ceil(K/128)]; both
+    float8_e4m3fn with uint8 (UE8M0) scales, I % 128 == 0. Returns (codes
+    [M, I], scales [M, I/128]) of act, then, with want_act, the BF16 act [M, I]
+    the codes were quantized from, and, with want_gu, BF16 [M, 2I] g and u for
+    swiglu_fp8_backward.
+    """
+    r = (_ext or load_tensors()).gemm_fp8_swiglu(a, a_scales, w13, w13_scales, want_act, want_gu,
+                                                 workspace, stream)
+    if type(r) is int:
+        raise Mxfp4Error(r, "mxfp4_gemm_fp8_swiglu")
+    return r
+
+
+def swiglu_fp8_backward(dact, gu, dtype=None, stream=None):
+    """The gradients of g and u from act's: bfloat16 dact [M, I] and gu
+    [M, 2I] (as gemm_fp8_swiglu's want_gu gives it), I % 128 == 0. dgu =
+    [dg, du] is quantized (dtype: float8_e4m3fn by default, or float8_e5m2;
+    uint8 scales) for both products that follow.
+
+    Returns (codes [M, 2I], scales [M, 2I/128], codes_t [2I, Mp], scales_t
+    [2I, ceil(M/128)]), Mp as quantize_fp8_2d's: with w13 and x quantized by
+    quantize_fp8_2d, dx = gemm_fp8(codes, scales, w13_t, w13_t_scales) and
+    dw13 = gemm_fp8(codes_t, scales_t, x_t, x_t_scales).
+    """
+    r = (_ext or load_tensors()).swiglu_fp8_backward(dact, gu, dtype, stream)
+    if type(r) is int:
+        raise Mxfp4Error(r, "mxfp4_swiglu_fp8_backward")
+    return r

@@ -1,6 +1,7 @@
-// Tensor layer of the few-token operators: checks torch tensors, allocates
-// outputs and workspaces from torch's allocator and calls the C ABI
-// (include/mxfp4_fewtoken.h) on torch's current stream or a given one.
+// Tensor layer of the few-token and FP8 operators: checks torch tensors,
+// allocates outputs and workspaces from torch's allocator and calls the C ABI
+// (include/mxfp4_fewtoken.h, include/mxfp4_fp8.h) on torch's current stream or
+// a given one.
 //
 // These calls run once per layer and token, where the host's time counts: the
 // same checks written in Python over ctypes cost 11.5 us a gemv, of which the
@@ -26,6 +27,7 @@
 #include <string>
 
 #include "../../include/mxfp4_fewtoken.h"
+#include "../../include/mxfp4_fp8.h"
 
 namespace {
 
@@ -35,6 +37,8 @@ std::string dtype_name(at::ScalarType t) {
     case at::kFloat: return "torch.float32";
     case at::kByte: return "torch.uint8";
     case at::kInt: return "torch.int32";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
+    case at::kFloat8_e5m2: return "torch.float8_e5m2";
     default: return std::string("torch ") + c10::toString(t);
   }
 }
@@ -169,7 +173,7 @@ int out_code(at::ScalarType t) { return t == at::kFloat ? MXFP4_OUT_FP32 : MXFP4
 // once the call has been enqueued.
 class Workspace {
  public:
-  Workspace(PyObject* o, int64_t bytes, const Rows& x, const Stream& stream) {
+  Workspace(PyObject* o, int64_t bytes, c10::DeviceIndex device, const Stream& stream) {
     if (o == Py_None) {
       if (bytes > 0)
         own_ = c10::hip::HIPCachingAllocator::raw_alloc_with_stream(
@@ -180,7 +184,7 @@ class Workspace {
     check_dtype(t, "workspace", at::kByte);
     TORCH_CHECK_VALUE(t.is_cuda(), "workspace must be a device tensor");
     TORCH_CHECK_VALUE(t.is_contiguous(), "workspace must be contiguous (row-major)");
-    TORCH_CHECK_VALUE(t.get_device() == x.device, "workspace must be on the current device");
+    TORCH_CHECK_VALUE(t.get_device() == device, "workspace must be on the current device");
     TORCH_CHECK_VALUE(t.numel() >= bytes, "workspace must hold ", bytes, " bytes, got ",
                       t.numel());
     given_ = t.data_ptr();
@@ -239,7 +243,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Stream stream = stream_of(a[7], x.device);
   Output ids = output(a[4], "ids", {T, k}, at::kInt, x, stream);
   Output weights = output(a[5], "weights", {T, k}, at::kFloat, x, stream);
-  const Workspace ws(a[6], bytes, x, stream);
+  const Workspace ws(a[6], bytes, x.device, stream);
   Py_BEGIN_ALLOW_THREADS;
   rc = mxfp4_moe_route(x.t.const_data_ptr(), x.ld, router.const_data_ptr(), T, H, E, k,
                        renormalize, ids.t.data_ptr(), weights.t.data_ptr(), ws.ptr(),
@@ -276,7 +280,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (rc) return PyLong_FromLong(rc);
   const Stream stream = stream_of(a[10], x.device);
   Output y = output(a[8], "out", {T, H}, type, x, stream);
-  const Workspace ws(a[9], bytes, x, stream);
+  const Workspace ws(a[9], bytes, x.device, stream);
   Py_BEGIN_ALLOW_THREADS;
   rc = mxfp4_moe(x.t.const_data_ptr(), x.ld, ids.const_data_ptr(), weights.const_data_ptr(),
                  c13.const_data_ptr(), s13.const_data_ptr(), c2.const_data_ptr(),
@@ -284,6 +288,233 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  ws.ptr(), stream.handle);
   Py_END_ALLOW_THREADS;
   return rc ? PyLong_FromLong(rc) : y.result();
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------------- FP8
+constexpr int64_t kFp8Block = 128;
+int64_t blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// A dtype argument, or `otherwise` for None.
+at::ScalarType dtype_of(PyObject* o, const char* name, at::ScalarType otherwise) {
+  if (o == Py_None) return otherwise;
+  TORCH_CHECK_TYPE(THPDtype_Check(o), name, " must be a torch.dtype");
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+at::ScalarType fp8_dtype(PyObject* o) {
+  const at::ScalarType t = dtype_of(o, "dtype", at::kFloat8_e4m3fn);
+  TORCH_CHECK_TYPE(t == at::kFloat8_e4m3fn || t == at::kFloat8_e5m2,
+                   "dtype must be torch.float8_e4m3fn or torch.float8_e5m2");
+  return t;
+}
+
+int fp8_code(at::ScalarType t) { return t == at::kFloat8_e5m2 ? MXFP4_FP8_E5M2 : MXFP4_FP8_E4M3; }
+int scale_code(at::ScalarType t) { return t == at::kFloat ? MXFP4_SCALE_FP32 : MXFP4_SCALE_UE8M0; }
+
+// A 2-D FP8 tensor on the current device, row-major.
+struct Codes {
+  const at::Tensor& t;
+  int64_t rows, cols;
+  at::ScalarType type;
+  c10::DeviceIndex device;
+};
+
+Codes codes_of(PyObject* o, const char* name, bool e5m2) {
+  const at::Tensor& t = tensor(o, name);
+  const at::ScalarType type = t.scalar_type();
+  TORCH_CHECK_TYPE(type == at::kFloat8_e4m3fn || (e5m2 && type == at::kFloat8_e5m2), name,
+                   " must be torch.float8_e4m3fn", e5m2 ? " or torch.float8_e5m2" : "", ", got ",
+                   dtype_name(type));
+  TORCH_CHECK_VALUE(t.dim() == 2, name, " must be 2-D");
+  TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a device tensor");
+  TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous (row-major)");
+  TORCH_CHECK_VALUE(t.get_device() == c10::hip::current_device(), name,
+                    " must be on the current device");
+  return {t, t.size(0), t.size(1), type, t.get_device()};
+}
+
+Output output(PyObject* out, const char* name, std::initializer_list<int64_t> shape,
+              at::ScalarType dtype, const Codes& x, const Stream& stream) {
+  if (out == Py_None)
+    return {stream.empty(at::IntArrayRef(shape.begin(), shape.size()), x.t, dtype), nullptr};
+  return {checked(out, name, dtype, shape, x.device), out};
+}
+
+PyObject* tuple_of(std::initializer_list<Output*> parts) {
+  PyObject* all = PyTuple_New((Py_ssize_t)parts.size());
+  if (!all) throw python_error();
+  Py_ssize_t i = 0;
+  for (Output* p : parts) PyTuple_SET_ITEM(all, i++, p->result());
+  return all;
+}
+
+bool truth(PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw python_error();
+  return t == 1;
+}
+
+int64_t integer(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+// What both quantizers check of x and their options, and the sizes.
+struct Quantize {
+  Rows x;
+  int64_t block;
+  at::ScalarType type, scale;
+
+  Quantize(PyObject* ox, PyObject* oblock, PyObject* odtype, PyObject* oscale)
+      : x(rows_of(ox, "x")), block(integer(oblock)), type(fp8_dtype(odtype)),
+        scale(dtype_of(oscale, "scale_dtype", at::kByte)) {
+    TORCH_CHECK_TYPE(scale == at::kByte || scale == at::kFloat,
+                     "scale_dtype must be torch.uint8 or torch.float32");
+    TORCH_CHECK_VALUE(block == 1 || block == kFp8Block, "block_rows must be 1 or 128");
+    TORCH_CHECK_VALUE(x.rows > 0 && x.cols > 0 && x.cols % 16 == 0,
+                      "x must be [M, K] with M > 0 and K a multiple of 16, got ",
+                      shape_text(x.t.sizes()));
+  }
+  int64_t scale_rows(int64_t rows) const { return block == 1 ? rows : blocks(rows); }
+};
+
+// quantize_fp8(x, block_rows, dtype, scale_dtype, codes, scales, stream)
+PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need(n, 7);
+  const Quantize q(a[0], a[1], a[2], a[3]);
+  const int64_t M = q.x.rows, K = q.x.cols;
+  const Stream stream = stream_of(a[6], q.x.device);
+  Output codes = output(a[4], "codes", {M, K}, q.type, q.x, stream);
+  Output scales = output(a[5], "scales", {q.scale_rows(M), blocks(K)}, q.scale, q.x, stream);
+  int rc = 0;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = mxfp4_quantize_fp8(q.x.t.const_data_ptr(), q.x.ld, M, K, q.block, fp8_code(q.type),
+                          scale_code(q.scale), codes.t.data_ptr(), scales.t.data_ptr(),
+                          stream.handle);
+  Py_END_ALLOW_THREADS;
+  return rc ? PyLong_FromLong(rc) : tuple_of({&codes, &scales});
+  END_HANDLE_TH_ERRORS
+}
+
+// quantize_fp8_2d(x, block_rows, dtype, scale_dtype, stream)
+PyObject* quantize_fp8_2d(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need(n, 5);
+  const Quantize q(a[0], a[1], a[2], a[3]);
+  const int64_t M = q.x.rows, K = q.x.cols;
+  const Stream stream = stream_of(a[4], q.x.device);
+  Output codes = output(Py_None, "codes", {M, K}, q.type, q.x, stream);
+  Output scales = output(Py_None, "scales", {q.scale_rows(M), blocks(K)}, q.scale, q.x, stream);
+  Output codes_t = output(Py_None, "codes_t", {K, up16(M)}, q.type, q.x, stream);
+  Output scales_t =
+      output(Py_None, "scales_t", {q.scale_rows(K), blocks(M)}, q.scale, q.x, stream);
+  int rc = 0;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = mxfp4_quantize_fp8_2d(q.x.t.const_data_ptr(), q.x.ld, M, K, q.block, fp8_code(q.type),
+                             scale_code(q.scale), codes.t.data_ptr(), scales.t.data_ptr(),
+                             codes_t.t.data_ptr(), scales_t.t.data_ptr(), stream.handle);
+  Py_END_ALLOW_THREADS;
+  return rc ? PyLong_FromLong(rc) : tuple_of({&codes, &scales, &codes_t, &scales_t});
+  END_HANDLE_TH_ERRORS
+}
+
+// gemm_fp8(a, a_scales, b, b_scales, out_dtype, out, stream)
+PyObject* gemm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need(n, 7);
+  const Codes x = codes_of(a[0], "a", true), w = codes_of(a[2], "b", false);
+  const int64_t M = x.rows, K = x.cols, N = w.rows, KB = blocks(K);
+  TORCH_CHECK_VALUE(w.cols == K, "b must have shape (N, ", K, "), got ",
+                    shape_text(w.t.sizes()));
+  const at::ScalarType scale = tensor(a[1], "a_scales").scalar_type();
+  TORCH_CHECK_TYPE(scale == at::kByte || scale == at::kFloat,
+                   "a_scales must be torch.uint8 or torch.float32, got ", dtype_name(scale));
+  const at::Tensor& xs = checked(a[1], "a_scales", scale, {M, KB}, x.device);
+  const int64_t rows = size_of(a[3], "b_scales", 2, 0);
+  const bool by_rows = rows == N && rows != blocks(N);
+  TORCH_CHECK_VALUE(!by_rows || scale == at::kByte,
+                    "float32 b_scales must be those of 128 x 128 blocks, ",
+                    shape_text({blocks(N), KB}));
+  const at::Tensor& ws =
+      checked(a[3], "b_scales", scale, {by_rows ? N : blocks(N), KB}, x.device);
+  const at::ScalarType type = out_type(a[4], a[5]);
+  const Stream stream = stream_of(a[6], x.device);
+  Output y = output(a[5], "out", {M, N}, type, x, stream);
+  int rc = 0;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = mxfp4_gemm_fp8(x.t.const_data_ptr(), fp8_code(x.type), xs.const_data_ptr(),
+                      w.t.const_data_ptr(), ws.const_data_ptr(), scale_code(scale),
+                      by_rows ? 1 : kFp8Block, M, N, K, out_code(type), y.t.data_ptr(),
+                      stream.handle);
+  Py_END_ALLOW_THREADS;
+  return rc ? PyLong_FromLong(rc) : y.result();
+  END_HANDLE_TH_ERRORS
+}
+
+// gemm_fp8_swiglu(a, a_scales, w13, w13_scales, want_act, want_gu, workspace,
+//                 stream)
+PyObject* gemm_fp8_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need(n, 8);
+  const Codes x = codes_of(a[0], "a", false), w = codes_of(a[2], "w13", false);
+  const int64_t M = x.rows, K = x.cols, I = w.rows / 2, KB = blocks(K);
+  TORCH_CHECK_VALUE(w.cols == K && I > 0 && w.rows % (2 * kFp8Block) == 0,
+                    "w13 must be [2 I, ", K, "] with I a multiple of 128, got ",
+                    shape_text(w.t.sizes()));
+  const at::Tensor& xs = checked(a[1], "a_scales", at::kByte, {M, KB}, x.device);
+  const at::Tensor& ws = checked(a[3], "w13_scales", at::kByte, {blocks(2 * I), KB}, x.device);
+  const bool want_act = truth(a[4]), want_gu = truth(a[5]);
+  int64_t bytes = 0;
+  int rc = mxfp4_gemm_fp8_swiglu_workspace(M, I, K, &bytes);
+  if (rc) return PyLong_FromLong(rc);
+  const Stream stream = stream_of(a[7], x.device);
+  Output codes = output(Py_None, "codes", {M, I}, at::kFloat8_e4m3fn, x, stream);
+  Output scales = output(Py_None, "scales", {M, I / kFp8Block}, at::kByte, x, stream);
+  Output act{at::Tensor(), nullptr}, gu{at::Tensor(), nullptr};
+  if (want_act) act = output(Py_None, "act", {M, I}, at::kBFloat16, x, stream);
+  if (want_gu) gu = output(Py_None, "gu", {M, 2 * I}, at::kBFloat16, x, stream);
+  const Workspace space(a[6], bytes, x.device, stream);
+  Py_BEGIN_ALLOW_THREADS;
+  rc = mxfp4_gemm_fp8_swiglu(x.t.const_data_ptr(), xs.const_data_ptr(), w.t.const_data_ptr(),
+                             ws.const_data_ptr(), M, I, K, codes.t.data_ptr(),
+                             scales.t.data_ptr(), want_act ? act.t.data_ptr() : nullptr,
+                             want_gu ? gu.t.data_ptr() : nullptr, space.ptr(), stream.handle);
+  Py_END_ALLOW_THREADS;
+  if (rc) return PyLong_FromLong(rc);
+  if (want_act && want_gu) return tuple_of({&codes, &scales, &act, &gu});
+  if (want_act) return tuple_of({&codes, &scales, &act});
+  return want_gu ? tuple_of({&codes, &scales, &gu}) : tuple_of({&codes, &scales});
+  END_HANDLE_TH_ERRORS
+}
+
+// swiglu_fp8_backward(dact, gu, dtype, stream)
+PyObject* swiglu_fp8_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  need(n, 4);
+  const Rows d = rows_of(a[0], "dact");
+  const int64_t M = d.rows, I = d.cols;
+  TORCH_CHECK_VALUE(d.t.is_contiguous(), "dact must be contiguous (row-major)");
+  TORCH_CHECK_VALUE(M > 0 && I > 0 && I % kFp8Block == 0,
+                    "dact must be [M, I] with M > 0 and I a multiple of 128, got ",
+                    shape_text(d.t.sizes()));
+  const at::Tensor& gu = checked(a[1], "gu", at::kBFloat16, {M, 2 * I}, d.device);
+  const at::ScalarType type = fp8_dtype(a[2]);
+  const Stream stream = stream_of(a[3], d.device);
+  Output codes = output(Py_None, "codes", {M, 2 * I}, type, d, stream);
+  Output scales = output(Py_None, "scales", {M, 2 * I / kFp8Block}, at::kByte, d, stream);
+  Output codes_t = output(Py_None, "codes_t", {2 * I, up16(M)}, type, d, stream);
+  Output scales_t = output(Py_None, "scales_t", {2 * I, blocks(M)}, at::kByte, d, stream);
+  int rc = 0;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = mxfp4_swiglu_fp8_backward(d.t.const_data_ptr(), gu.const_data_ptr(), M, I, fp8_code(type),
+                                 codes.t.data_ptr(), scales.t.data_ptr(), codes_t.t.data_ptr(),
+                                 scales_t.t.data_ptr(), stream.handle);
+  Py_END_ALLOW_THREADS;
+  return rc ? PyLong_FromLong(rc) : tuple_of({&codes, &scales, &codes_t, &scales_t});
   END_HANDLE_TH_ERRORS
 }
 
@@ -295,6 +526,11 @@ PyMethodDef methods[] = {
     {"gemv", fast(gemv), METH_FASTCALL, nullptr},
     {"moe_route", fast(moe_route), METH_FASTCALL, nullptr},
     {"moe", fast(moe), METH_FASTCALL, nullptr},
+    {"quantize_fp8", fast(quantize_fp8), METH_FASTCALL, nullptr},
+    {"quantize_fp8_2d", fast(quantize_fp8_2d), METH_FASTCALL, nullptr},
+    {"gemm_fp8", fast(gemm_fp8), METH_FASTCALL, nullptr},
+    {"gemm_fp8_swiglu", fast(gemm_fp8_swiglu), METH_FASTCALL, nullptr},
+    {"swiglu_fp8_backward", fast(swiglu_fp8_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxfp4.so")
 SOURCES = ["api.hip", "quantize.hip", "quantize_sr.hip", "quantize2d.hip", "gemm.hip",
            "gemm_skinny.hip", "shuffle.hip", "api_fewtoken.hip", "gemv.hip", "moe_route.hip",
-           "moe.hip", "api_fp8.hip", "quantize_fp8.hip", "gemm_fp8.hip", "gemm_fp8_small.hip", "swiglu_fp8.hip"]
+           "moe.hip", "api_fp8.hip", "quantize_fp8.hip", "gemm_fp8.hip",
+           "gemm_fp8_small.hip", "gemm_fp8_tile.hip", "swiglu_fp8.hip"]
 ARCH = "gfx950"
 
 

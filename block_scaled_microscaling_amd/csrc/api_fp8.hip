@@ -121,7 +121,7 @@ int mxfp4_gemm_fp8_swiglu_workspace(int64_t M, int64_t I, int64_t K, int64_t* by
     return MXFP4_EINVAL;
   if (!below_max_bytes(M, I, 4) || !below_max_bytes(2 * I, K) || !below_max_bytes(M, K))
     return MXFP4_EINVAL;
-  *bytes = mxfp4::gemm_fp8_swiglu_small(M, I) ? 2 * M * I : 0;
+  *bytes = mxfp4::gemm_fp8_swiglu_small(M, I, K) ? 2 * M * I : 0;
   return MXFP4_OK;
 }
 

@@ -89,6 +89,28 @@ __device__ __forceinline__ uint32_t fp8_pair_f32(uint32_t old, float a, float b,
                               __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(o, a, b, scale, kHigh));
 }
 
+// A lane's 16 bytes (8 BF16 values): their largest finite magnitude, biased;
+// the scale byte of a row's block held by 16 lanes; and their codes.
+__device__ __forceinline__ i16x2_t biased_chunk_max(u32x4_t v) {
+  const uint32_t a = v[0], b = v[1], c = v[2], d = v[3];
+  return max_pair(max_pair(biased_abs_pair(a), biased_abs_pair(b)),
+                  max_pair(biased_abs_pair(c), biased_abs_pair(d)));
+}
+template <Fp8Type kType>
+__device__ __forceinline__ uint32_t fp8_row_scale(u32x4_t v) {
+  const i16x2_t m = biased_chunk_max(v);
+  const int top = row16_max(max(max((int)m.x, (int)m.y), kAmaxBias));
+  return fp8_scale_byte_bf16<kType>((uint32_t)(top - kAmaxBias));
+}
+template <Fp8Type kType>
+__device__ __forceinline__ uint2 fp8_encode_chunk(u32x4_t v, float scale) {
+  const uint32_t a = v[0], b = v[1], c = v[2], d = v[3];
+  uint2 r;
+  r.x = fp8_pair_bf16<kType, true>(fp8_pair_bf16<kType, false>(0, a, scale), b, scale);
+  r.y = fp8_pair_bf16<kType, true>(fp8_pair_bf16<kType, false>(0, c, scale), d, scale);
+  return r;
+}
+
 // Scales as a kernel writes them: UE8M0 bytes or FP32.
 __device__ __forceinline__ void store_scale(void* scales, int64_t at, uint32_t byte, bool f32) {
   if (f32)
@@ -155,6 +177,44 @@ struct Fp8QuantArgs {
 hipError_t launch_quantize_fp8(const Fp8QuantArgs& a, int block_rows, Fp8Type type,
                                hipStream_t stream);
 
+// Tile p in the order of the workgroups: XCD x (every 8th workgroup) takes a
+// contiguous run of tiles, `group` tile rows at a time, so that the tiles that
+// run together on one XCD share rows of A and B in its L2.
+__device__ __forceinline__ void xcd_tile(int p, int tiles_m, int tiles_n, int group, int& tm,
+                                         int& tn) {
+  constexpr int kXcds = 8;
+  const int total = tiles_m * tiles_n;
+  const int each = total / kXcds, rem = total % kXcds;
+  const int xcd = p % kXcds;
+  const int at = xcd * each + min(xcd, rem) + p / kXcds;
+  const int width = group * tiles_n;
+  const int first = at / width * group, size = min(tiles_m - first, group);
+  const int in = at % width;
+  tm = first + in % size;
+  tn = in / size;
+}
+
+// Four UE8M0 bytes of scales from byte `at` of an array of at least four, the
+// first in the low byte; those past its end are of no meaning.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* scales, int64_t at, int64_t total) {
+  const int64_t p = min(at, total - 4);
+  uint32_t w;
+  __builtin_memcpy(&w, scales + p, 4);
+  return w >> (8 * (int)(at - p) & 31);
+}
+// The same of an array of any length.
+__device__ __forceinline__ uint32_t short_scale_word(const uint8_t* scales, int64_t at,
+                                                     int64_t total) {
+  if (total >= 4) return scale_word(scales, at, total);
+  uint32_t w = 0;
+  for (int i = 0; i < 4; ++i)
+    if (at + i < total) w |= (uint32_t)scales[at + i] << (8 * i);
+  return w;
+}
+
+// Where a DMA of chunks past K reads from.
+static __device__ __align__(16) const uint8_t kFp8Zeros[16] = {};
+
 // A GEMM's operands: A [M, K] of type a_type, B [N, K] E4M3, scales of both
 // UE8M0 or FP32, B's per 1 << b_shift rows (0 or 7). With glu, B is the
 // stacked [W_gate; W_up] and N = I, the activation's columns.
@@ -173,13 +233,22 @@ enum Fp8Out { kFp8Bf16 = 0, kFp8F32 = 1, kFp8Glu = 2 };
 hipError_t launch_gemm_fp8_small(const Fp8GemmArgs& a, Fp8Out out, Fp8Type a_type, bool scale_f32,
                                  hipStream_t stream);
 
+// BF16 results and kFp8Glu (with its quantize) of UE8M0 operands, on 256 x 256
+// tiles.
+struct Fp8ActOut {
+  uint8_t* codes;   // [M, I]
+  uint8_t* scales;  // [M, I / 128]
+};
+hipError_t launch_gemm_fp8_tile(const Fp8GemmArgs& a, Fp8Out out, Fp8Type a_type,
+                                const Fp8ActOut& act, hipStream_t stream);
+
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, Fp8Out out, Fp8Type a_type, bool scale_f32,
                            hipStream_t stream);
 
 // Whether the gate+up product of these sizes runs on the kernel for few rows,
 // which leaves act in BF16 (workspace: 2 M I bytes, where a.C is null) for a
 // quantize of its own.
-bool gemm_fp8_swiglu_small(int64_t M, int64_t I);
+bool gemm_fp8_swiglu_small(int64_t M, int64_t I, int64_t K);
 hipError_t launch_gemm_fp8_swiglu(const Fp8GemmArgs& a, uint8_t* codes, uint8_t* scales,
                                   void* workspace, hipStream_t stream);
 

@@ -33,40 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = 128;                    // rows of A and of B per workgroup
 constexpr int kRowBytes = kFp8Block;          // of one row in a K step
 constexpr int kSlotBytes = kTile * kRowBytes;  // 16 KiB an operand
-constexpr int kNumXcd = 8;
 constexpr int kGroupM = 8;
-
-__device__ __align__(16) const uint8_t kZeros[16] = {};
-
-// Tile p in the order of the workgroups: XCD x (every 8th workgroup) takes a
-// contiguous run of tiles, kGroupM tile rows at a time.
-__device__ __forceinline__ void tile_of(int p, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int total = tiles_m * tiles_n;
-  const int each = total / kNumXcd, rem = total % kNumXcd;
-  const int xcd = p % kNumXcd;
-  const int at = xcd * each + min(xcd, rem) + p / kNumXcd;
-  const int width = kGroupM * tiles_n;
-  const int group = at / width;
-  const int first = group * kGroupM, size = min(tiles_m - first, kGroupM);
-  const int in = at - group * width;
-  tm = first + in % size;
-  tn = in / size;
-}
-
-// Four UE8M0 bytes of scales from byte `at`, the first in the low byte; those
-// past the array are not read (and not used).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* scales, int64_t at, int64_t total) {
-  if (total >= 4) {
-    const int64_t p = min(at, total - 4);
-    uint32_t w;
-    __builtin_memcpy(&w, scales + p, 4);
-    return at - p >= 4 ? 0 : w >> (8 * (int)(at - p));
-  }
-  uint32_t w = 0;
-  for (int i = 0; i < 4; ++i)
-    if (at + i < total) w |= (uint32_t)scales[at + i] << (8 * i);
-  return w;
-}
 
 typedef float v16_t __attribute__((ext_vector_type(16)));
 
@@ -101,7 +68,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
   const int id = workgroup_id(tiles_m * tiles_n);
   if (id < 0) return;
   int tm, tn;
-  tile_of(id, tiles_m, tiles_n, tm, tn);
+  xcd_tile(id, tiles_m, tiles_n, kGroupM, tm, tn);
   const int row0 = tm * kTile;
   const int col0 = tn * (kGlu ? kTile / 2 : kTile);
 
@@ -138,7 +105,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
     for (int q = 0; q < 4; ++q) {
       const uint8_t* ga = from_a[q] + k;
       const uint8_t* gb = from_b[q] + k;
-      if (tail && 16 * chunk[q & 1] >= last_bytes) ga = gb = kZeros;
+      if (tail && 16 * chunk[q & 1] >= last_bytes) ga = gb = kFp8Zeros;
       dma16(ga, to_a + 1024 * q);
       dma16(gb, to_b + 1024 * q);
     }
@@ -165,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
         b[i] = static_cast<const uint32_t*>(p.Bs)[sb_at[i] + kb];
       } else {
         a[i] = scale_word(static_cast<const uint8_t*>(p.As), sa_at[i] + kb, sa_total);
-        b[i] = scale_word(static_cast<const uint8_t*>(p.Bs), sb_at[i] + kb, sb_total);
+        b[i] = short_scale_word(static_cast<const uint8_t*>(p.Bs), sb_at[i] + kb, sb_total);
       }
     }
   };
@@ -400,19 +367,32 @@ hipError_t launch_typed(const Fp8GemmArgs& a, Fp8Out out, bool f32, hipStream_t 
 
 constexpr int kSmallMaxM = 64;
 
+// Whether a product runs on 256 x 256 tiles: where they fill the chip. (B's
+// scales are then read four bytes at a time.)
+bool big_tiles(int64_t M, int64_t N, int64_t K) {
+  return M > 256 && ((M + 255) / 256) * ((N + 255) / 256) > 128 &&
+         (N + 127) / 128 * ((K + 127) / 128) >= 4;
+}
+
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, Fp8Out out, Fp8Type a_type, bool scale_f32,
                            hipStream_t stream) {
   if (a.M <= kSmallMaxM) return launch_gemm_fp8_small(a, out, a_type, scale_f32, stream);
+  if (out == kFp8Bf16 && !scale_f32 && big_tiles(a.M, a.N, a.K))
+    return launch_gemm_fp8_tile(a, out, a_type, Fp8ActOut{}, stream);
   return a_type == kE4M3 ? launch_typed<kE4M3>(a, out, scale_f32, stream)
                          : launch_typed<kE5M2>(a, out, scale_f32, stream);
 }
 
-bool gemm_fp8_swiglu_small(int64_t, int64_t) { return true; }
+bool gemm_fp8_swiglu_small(int64_t M, int64_t I, int64_t K) {
+  return !big_tiles(M, 2 * I, K);
+}
 
 hipError_t launch_gemm_fp8_swiglu(const Fp8GemmArgs& a, uint8_t* codes, uint8_t* scales,
                                   void* workspace, hipStream_t stream) {
+  if (!gemm_fp8_swiglu_small(a.M, a.N, a.K))
+    return launch_gemm_fp8_tile(a, kFp8Glu, kE4M3, Fp8ActOut{codes, scales}, stream);
   Fp8GemmArgs g = a;
   if (!g.C) g.C = workspace;
   const hipError_t e = a.M <= kSmallMaxM

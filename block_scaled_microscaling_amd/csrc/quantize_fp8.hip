@@ -32,21 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = kFp8Block;
 constexpr int kMaxGrid = 1 << 20;  // workgroups; the kernels stride over the rest
 
-__device__ __forceinline__ i16x2_t chunk_max(u32x4_t v) {
-  const uint32_t a = v[0], b = v[1], c = v[2], d = v[3];
-  return max_pair(max_pair(biased_abs_pair(a), biased_abs_pair(b)),
-                  max_pair(biased_abs_pair(c), biased_abs_pair(d)));
-}
 __device__ __forceinline__ int pair_max(i16x2_t m) { return max((int)m.x, (int)m.y); }
-
-template <Fp8Type kType>
-__device__ __forceinline__ uint2 encode_chunk(u32x4_t v, float scale) {
-  const uint32_t a = v[0], b = v[1], c = v[2], d = v[3];
-  uint2 r;
-  r.x = fp8_pair_bf16<kType, true>(fp8_pair_bf16<kType, false>(0, a, scale), b, scale);
-  r.y = fp8_pair_bf16<kType, true>(fp8_pair_bf16<kType, false>(0, c, scale), d, scale);
-  return r;
-}
 
 // Blocks go in flat order over [M, ceil(K / 128)]; kFlat: rows are whole
 // blocks and lie one behind the other, so that the order is that of memory.
@@ -80,9 +66,8 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_rows_kernel(Fp8QuantArg
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int64_t b = b0 + i * kGroups + g;
-      const int top = row16_max(max(pair_max(chunk_max(v[i])), kAmaxBias));
-      const uint32_t byte = fp8_scale_byte_bf16<kType>((uint32_t)(top - kAmaxBias));
-      const uint2 code = encode_chunk<kType>(v[i], fp8_scale_value(byte));
+      const uint32_t byte = fp8_row_scale<kType>(v[i]);
+      const uint2 code = fp8_encode_chunk<kType>(v[i], fp8_scale_value(byte));
       if (in[i]) *reinterpret_cast<uint2*>(p.codes + out[i]) = code;
       if (c == 0 && b < blocks) store_scale(p.scales, b, byte, p.scale_f32);
     }
@@ -149,12 +134,11 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_tile_kernel(Fp8QuantArg
     for (int i = 0; i < 8; ++i) {
       uint32_t byte = square;
       if constexpr (!kSquare) {
-        const int top = row16_max(max(pair_max(chunk_max(v[i])), kAmaxBias));
-        byte = fp8_scale_byte_bf16<kType>((uint32_t)(top - kAmaxBias));
+        byte = fp8_row_scale<kType>(v[i]);
         if (c == 0 && m0 + i < p.M)
           store_scale(p.scales, (m0 + i) * kblocks + kb, byte, p.scale_f32);
       }
-      const uint2 code = encode_chunk<kType>(v[i], fp8_scale_value(byte));
+      const uint2 code = fp8_encode_chunk<kType>(v[i], fp8_scale_value(byte));
       if (m0 + i < p.M && k0 < p.K)
         *reinterpret_cast<uint2*>(p.codes + (m0 + i) * p.K + k0) = code;
     }

@@ -314,3 +314,63 @@ def test_mlp_forward_and_backward(M, H, I):
         got, want = got.double().cpu(), want
         assert got.shape == want.shape
         assert torch.linalg.norm(got - want) <= 0.15 * torch.linalg.norm(want)
+
+
+# ------------------------------------------------------------- large tiles
+def check_product_on_gpu(got, a, sa, b, sb, block, fp8_path):
+    """check_product in 64 bits on the GPU, for sizes that take large tiles."""
+    def vals(c, s, rows):
+        s = s.double() if s.dtype == torch.float32 else torch.exp2(s.double() - 127)
+        s = s.repeat_interleave(rows, 0)[: c.shape[0]].repeat_interleave(128, 1)[:, : c.shape[1]]
+        return c.double() * s
+    K = a.shape[1]
+    va, vb = vals(a, sa, 1), vals(b, sb, block)
+    C, S = va @ vb.t().contiguous(), va.abs() @ vb.abs().t().contiguous()
+    tol = (K + 8) * 2.0 ** -24 * S
+    if got.dtype == torch.bfloat16:
+        if fp8_path:
+            def tops(v):
+                pad = -v.shape[1] % 8
+                return torch.nn.functional.pad(v.abs(), (0, pad)).view(v.shape[0], -1, 8).amax(2)
+            tol = tol + 8 * 2.0 ** -13 * (tops(va) @ tops(vb).t().contiguous())
+        tol = tol + fp8.BF16_HALF_STEP * (C.abs() + tol)
+    bad = ((got.double() - C).abs() > tol) | got.isnan()
+    assert not bad.any(), f"{int(bad.sum())} outside, first {bad.nonzero()[:4].tolist()}"
+    return C, va, vb
+
+
+BIG = [(3200, 2900, 16), (2817, 3333, 128), (3201, 3137, 400), (4096, 2304, 512),
+       (2900, 3211, 640), (2818, 3000, 784), (2817, 2944, 1168)]
+
+
+@pytest.mark.parametrize("M,N,K", BIG)
+@pytest.mark.parametrize("scales,block", [("ue8m0", 128), ("ue8m0", 1), ("fp32", 128)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_gemm_of_many_tiles(M, N, K, scales, block, out):
+    kind = KINDS[(M + N + block) % 2]
+    announce(f"gemm_fp8 {M}x{N}x{K} {kind} {scales}/{block} {out}")
+    a, sa, _ = operand(M, K, 1, kind, scales, M + K)
+    b, sb, _ = operand(N, K, block, "e4m3", scales, N + K + 1, std=0.02)
+    got = mx.gemm_fp8(a, sa, b, sb, out_dtype=out)
+    check_product_on_gpu(got, a, sa, b, sb, block, True)
+
+
+@pytest.mark.parametrize("M,H,I", [(2900, 16, 1536), (4096, 512, 1152), (2817, 656, 1664)])
+def test_swiglu_of_many_tiles(M, H, I):
+    announce(f"gemm_fp8_swiglu {M}x{H}x{I}")
+    a, sa, _ = operand(M, H, 1, "e4m3", "ue8m0", M + H)
+    w, sw, _ = operand(2 * I, H, 128, "e4m3", "ue8m0", I, std=2.0 / np.sqrt(H))
+    codes, scales, act, gu = mx.gemm_fp8_swiglu(a, sa, w, sw, want_act=True, want_gu=True)
+    C, va, vw = check_product_on_gpu(gu, a, sa, w, sw, 128, True)
+    off = fp8.exact_tolerance(*fp8.product(va.cpu().numpy(), vw.cpu().numpy()), H)
+    off = off + fp8.grouped_tolerance(va.cpu().numpy(), vw.cpu().numpy())
+    C = C.cpu().numpy()
+    ref = fp8.swiglu(C[:, :I], C[:, I:])
+    tol = fp8.swiglu_tolerance(C[:, :I], C[:, I:], off[:, :I], off[:, I:])
+    tol = tol + fp8.BF16_HALF_STEP * (np.abs(ref) + tol)
+    got = act.double().cpu().numpy()
+    assert (np.abs(got - ref) <= tol).all()
+    want = fp8.quantize(got, 1, "e4m3")
+    for again in ((codes, scales), mx.gemm_fp8_swiglu(a, sa, w, sw)):
+        assert np.array_equal(bytes_of(again[0]), want[0])
+        assert np.array_equal(again[1].cpu().numpy(), want[1])

@@ -13,8 +13,8 @@
 // Data movement. A K step is one block of 128: 128 bytes a row, a whole line,
 // two slices of 64 for the instruction. Tiles go global -> LDS by DMA (8 rows an
 // instruction, addresses from a wave-uniform base and per-lane offsets prepared
-// once), two steps resident (128 KiB), in rows of eight 16-byte chunks
-// XOR-swizzled by the row, so that fragment reads fall on all banks.
+// once) into two slots of A and three of B (160 KiB), in rows of eight 16-byte
+// chunks XOR-swizzled by the row, so that fragment reads fall on all banks.
 //
 // Schedule of a step. A slice runs in two halves, B tiles 0 and 1 with all four
 // of A, then 2 and 3, so that every fragment has one set of registers (64) and
@@ -22,7 +22,8 @@
 // done at once, A's one by one behind their last use. All reads of a step are
 // done after the first half of its second slice; there the waves meet (the next
 // step's tiles have landed, this step's may be overwritten), and the DMAs of the
-// step after next go out over the next 16 instructions, a whole step ahead.
+// step after next go out over the next 16 instructions: A's a whole step ahead,
+// B's, which have a third slot, nearly two.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -44,7 +45,7 @@ struct Ctx {
   const uint8_t* base_a;        // wave-uniform, less kBias
   const uint8_t* base_b;
   uint32_t lds;                 // of this wave's rows in slot 0 of A
-  uint32_t fa[4], fb[4];        // fragment reads of quarter q of a step
+  uint32_t fa[4], fb[4];        // fragment reads of quarter q of a step, slot 0
   int last;                     // last K step
   int tail_bytes;               // of the last step, where K % 128 != 0
   int chunk[2];                 // the chunk a lane fetches, rows at 0 and 8 mod 16
@@ -67,10 +68,9 @@ __device__ __forceinline__ void dma_pair(const uint8_t* base, uint32_t off0, uin
 
 // kOp: 0 = A, 1 = B. A last step that ends inside a block takes its chunks past
 // K from a line of zeros.
-template <int kOp, int Q0, int S, bool kTail>
-__device__ __forceinline__ void load_pair(const Ctx& c, int kb) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(c.lds + (2 * kOp + S) * kSlot +
-                                                     (Q0 / 4) * 4096);
+template <int kOp, int Q0, bool kTail>
+__device__ __forceinline__ void load_pair(const Ctx& c, int kb, uint32_t slot) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(c.lds + slot + (Q0 / 4) * 4096);
   const uint8_t* base = (kOp ? c.base_b : c.base_a) + (int64_t)kb * kRowBytes;
   const uint32_t o0 = kOp ? c.off_b[Q0] : c.off_a[Q0];
   const uint32_t o1 = kOp ? c.off_b[Q0 + 1] : c.off_a[Q0 + 1];
@@ -94,10 +94,10 @@ struct Frag {
   u32x4_t lo, hi;
 };
 
-template <int S, int kSlice>
+template <int kSlice>
 __device__ __forceinline__ void read_frag(const uint8_t* lds, const uint32_t (&at)[4], int tile,
                                           Frag& f) {
-  const uint8_t* p = lds + S * kSlot + tile * 32 * kRowBytes;
+  const uint8_t* p = lds + tile * 32 * kRowBytes;
   f.lo = *reinterpret_cast<const u32x4_t*>(p + at[2 * kSlice]);
   f.hi = *reinterpret_cast<const u32x4_t*>(p + at[2 * kSlice + 1]);
 }
@@ -148,71 +148,81 @@ __device__ __forceinline__ void load_scales(const ScaleRows<kNB>& w, int kb, Sca
   for (int j = 0; j < kNB; ++j) s.b[j] = scale_word(w.Bs, w.b[j] + kb, w.b_total);
 }
 
-// One K step T in slot S, P = T % 4. Fragments of its first slice are there but
-// for A's tile 3.
+// Offsets of B's three slots: of steps T, T + 1 and T + 2.
+struct Ring {
+  uint32_t now, next, free;
+};
+
+// One K step T, P = T % 4, A in slot P % 2. Fragments of its first slice are
+// there but for A's tile 3.
 template <Fp8Type kA, int kNB, bool kTail, int P>
 __device__ __forceinline__ void k_step(const Ctx& c, const uint8_t* lds, v16f_t (&acc)[4][4],
                                        Frag (&a)[4], Frag (&b)[4], const ScaleRows<kNB>& rows,
-                                       Scales<kNB>& s, Scales<kNB>& next, int T) {
+                                       Scales<kNB>& s, Scales<kNB>& next, Ring& ring, int T) {
   constexpr int S = P & 1;
-  const int k1 = min(T + 1, c.last), k2 = min(T + 2, c.last);
+  const uint8_t* lds_a = lds + S * kSlot;
+  const uint8_t* lds_a1 = lds + (1 - S) * kSlot;
+  const uint8_t* lds_b = lds + ring.now;
+  const uint8_t* lds_b1 = lds + ring.next;
+  const int k2 = min(T + 2, c.last);
   const auto sb = [&](int j) { return s.b[kNB == 1 ? 0 : kNB == 2 ? j & 1 : j]; };
 #define MXFP4_MMA(i, j) mma<kA>(acc[i][j], b[j], a[i], sb(j), s.a[i])
-  // Slice 0, B tiles 0, 1; the DMAs of step T + 1's B.
+  // Slice 0, B tiles 0, 1; the DMAs of step T + 2's B.
   MXFP4_MMA(0, 0);
   MXFP4_MMA(0, 1);
-  read_frag<S, 0>(lds, c.fa, 3, a[3]);
-  load_pair<1, 0, 1 - S, kTail>(c, k1);
+  read_frag<0>(lds_a, c.fa, 3, a[3]);
+  load_pair<1, 0, kTail>(c, k2, ring.free);
   group_end<2>();
   MXFP4_MMA(1, 0);
   MXFP4_MMA(1, 1);
-  read_frag<S, 0>(lds, c.fb, 2, b[2]);
-  load_pair<1, 2, 1 - S, kTail>(c, k1);
+  read_frag<0>(lds_b, c.fb, 2, b[2]);
+  load_pair<1, 2, kTail>(c, k2, ring.free);
   group_end<2>();
   MXFP4_MMA(2, 0);
   MXFP4_MMA(2, 1);
-  read_frag<S, 0>(lds, c.fb, 3, b[3]);
-  load_pair<1, 4, 1 - S, kTail>(c, k1);
+  read_frag<0>(lds_b, c.fb, 3, b[3]);
+  load_pair<1, 4, kTail>(c, k2, ring.free);
   group_end<2>();
   MXFP4_MMA(3, 0);
   MXFP4_MMA(3, 1);
-  load_pair<1, 6, 1 - S, kTail>(c, k1);
+  load_pair<1, 6, kTail>(c, k2, ring.free);
   group_end<0>();
   // B tiles 2, 3.
   MXFP4_MMA(0, 2);
   MXFP4_MMA(0, 3);
-  read_frag<S, 1>(lds, c.fb, 0, b[0]);
+  read_frag<1>(lds_b, c.fb, 0, b[0]);
   group_end<2>();
   MXFP4_MMA(1, 2);
   MXFP4_MMA(1, 3);
-  read_frag<S, 1>(lds, c.fb, 1, b[1]);
-  read_frag<S, 1>(lds, c.fa, 0, a[0]);
+  read_frag<1>(lds_b, c.fb, 1, b[1]);
+  read_frag<1>(lds_a, c.fa, 0, a[0]);
   group_end<4>();
   MXFP4_MMA(2, 2);
   MXFP4_MMA(2, 3);
-  read_frag<S, 1>(lds, c.fa, 1, a[1]);
+  read_frag<1>(lds_a, c.fa, 1, a[1]);
   group_end<2>();
   MXFP4_MMA(3, 2);
   MXFP4_MMA(3, 3);
-  read_frag<S, 1>(lds, c.fa, 2, a[2]);
+  read_frag<1>(lds_a, c.fa, 2, a[2]);
   group_end<2>();
   // Slice 1.
   MXFP4_MMA(0, 0);
   MXFP4_MMA(0, 1);
-  read_frag<S, 1>(lds, c.fa, 3, a[3]);
+  read_frag<1>(lds_a, c.fa, 3, a[3]);
   group_end<2>();
   MXFP4_MMA(1, 0);
   MXFP4_MMA(1, 1);
-  read_frag<S, 1>(lds, c.fb, 2, b[2]);
+  read_frag<1>(lds_b, c.fb, 2, b[2]);
   group_end<2>();
   MXFP4_MMA(2, 0);
   MXFP4_MMA(2, 1);
-  read_frag<S, 1>(lds, c.fb, 3, b[3]);
+  read_frag<1>(lds_b, c.fb, 3, b[3]);
   group_end<2>();
   MXFP4_MMA(3, 0);
   MXFP4_MMA(3, 1);
   group_end<0>();
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  // All but the last 8 loads (step T + 2's B): step T + 1 has landed.
+  asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   MXFP4_FENCE();
   if constexpr (P == 3) {
     // The next words were loaded in the step before: landed by now.
@@ -221,30 +231,31 @@ __device__ __forceinline__ void k_step(const Ctx& c, const uint8_t* lds, v16f_t 
 #pragma unroll
     for (int j = 0; j < kNB; ++j) asm volatile("" : "+v"(next.b[j]));
   }
-  if constexpr (P == 2) load_scales(rows, T + 2, next);  // past the last: not used
+  if constexpr (P == 1) load_scales(rows, T + 3, next);  // past the last: not used
   // B tiles 2, 3; the first fragments of step T + 1, the DMAs of step T + 2's A.
   MXFP4_MMA(0, 2);
   MXFP4_MMA(0, 3);
-  read_frag<1 - S, 0>(lds, c.fb, 0, b[0]);
-  load_pair<0, 0, S, kTail>(c, k2);
+  read_frag<0>(lds_b1, c.fb, 0, b[0]);
+  load_pair<0, 0, kTail>(c, k2, S * kSlot);
   group_end<2>();
   MXFP4_MMA(1, 2);
   MXFP4_MMA(1, 3);
-  read_frag<1 - S, 0>(lds, c.fb, 1, b[1]);
-  read_frag<1 - S, 0>(lds, c.fa, 0, a[0]);
-  load_pair<0, 2, S, kTail>(c, k2);
+  read_frag<0>(lds_b1, c.fb, 1, b[1]);
+  read_frag<0>(lds_a1, c.fa, 0, a[0]);
+  load_pair<0, 2, kTail>(c, k2, S * kSlot);
   group_end<4>();
   MXFP4_MMA(2, 2);
   MXFP4_MMA(2, 3);
-  read_frag<1 - S, 0>(lds, c.fa, 1, a[1]);
-  load_pair<0, 4, S, kTail>(c, k2);
+  read_frag<0>(lds_a1, c.fa, 1, a[1]);
+  load_pair<0, 4, kTail>(c, k2, S * kSlot);
   group_end<2>();
   MXFP4_MMA(3, 2);
   MXFP4_MMA(3, 3);
-  read_frag<1 - S, 0>(lds, c.fa, 2, a[2]);
-  load_pair<0, 6, S, kTail>(c, k2);
+  read_frag<0>(lds_a1, c.fa, 2, a[2]);
+  load_pair<0, 6, kTail>(c, k2, S * kSlot);
   group_end<2>();
 #undef MXFP4_MMA
+  ring = Ring{ring.next, ring.free, ring.now};
   if constexpr (P == 3) {
     s = next;
   } else {
@@ -260,7 +271,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
 void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act) {
   constexpr bool kGlu = kOut == kFp8Glu;
   constexpr int kNB = kRowsB ? 4 : kGlu ? 2 : 1;
-  __shared__ __align__(16) uint8_t lds[4 * kSlot];  // A's slots 0, 1, then B's
+  __shared__ __align__(16) uint8_t lds[5 * kSlot];  // A's slots 0, 1, then B's 0, 1, 2
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -306,7 +317,7 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     c.fa[q] = (uint32_t)(128 * wy + r) * kRowBytes + ((32u * q) ^ x);
-    c.fb[q] = 2 * kSlot + (uint32_t)(128 * wx + r) * kRowBytes + ((32u * q) ^ x);
+    c.fb[q] = (uint32_t)(128 * wx + r) * kRowBytes + ((32u * q) ^ x);
   }
 
   ScaleRows<kNB> rows;
@@ -325,41 +336,46 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
   Scales<kNB> s, next;
   load_scales(rows, 0, s);
   next = s;
+  Ring ring{2 * kSlot, 3 * kSlot, 4 * kSlot};
   const int k1 = min(1, c.last);
-  load_pair<0, 0, 0, kTail>(c, 0);
-  load_pair<0, 2, 0, kTail>(c, 0);
-  load_pair<0, 4, 0, kTail>(c, 0);
-  load_pair<0, 6, 0, kTail>(c, 0);
-  load_pair<1, 0, 0, kTail>(c, 0);
-  load_pair<1, 2, 0, kTail>(c, 0);
-  load_pair<1, 4, 0, kTail>(c, 0);
-  load_pair<1, 6, 0, kTail>(c, 0);
-  load_pair<0, 0, 1, kTail>(c, k1);
-  load_pair<0, 2, 1, kTail>(c, k1);
-  load_pair<0, 4, 1, kTail>(c, k1);
-  load_pair<0, 6, 1, kTail>(c, k1);
+  load_pair<0, 0, kTail>(c, 0, 0);
+  load_pair<0, 2, kTail>(c, 0, 0);
+  load_pair<0, 4, kTail>(c, 0, 0);
+  load_pair<0, 6, kTail>(c, 0, 0);
+  load_pair<1, 0, kTail>(c, 0, ring.now);
+  load_pair<1, 2, kTail>(c, 0, ring.now);
+  load_pair<1, 4, kTail>(c, 0, ring.now);
+  load_pair<1, 6, kTail>(c, 0, ring.now);
+  load_pair<1, 0, kTail>(c, k1, ring.next);
+  load_pair<1, 2, kTail>(c, k1, ring.next);
+  load_pair<1, 4, kTail>(c, k1, ring.next);
+  load_pair<1, 6, kTail>(c, k1, ring.next);
+  load_pair<0, 0, kTail>(c, k1, kSlot);
+  load_pair<0, 2, kTail>(c, k1, kSlot);
+  load_pair<0, 4, kTail>(c, k1, kSlot);
+  load_pair<0, 6, kTail>(c, k1, kSlot);
   v16f_t acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v16f_t{};
-  // Step 0 has landed; the 8 DMAs of step 1's A may be under way.
-  asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+  // Step 0 has landed; the 16 DMAs of step 1 may be under way.
+  asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
   Frag a[4], b[4];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) read_frag<0, 0>(lds, c.fa, i, a[i]);
+  for (int i = 0; i < 3; ++i) read_frag<0>(lds, c.fa, i, a[i]);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) read_frag<0, 0>(lds, c.fb, j, b[j]);
+  for (int j = 0; j < 2; ++j) read_frag<0>(lds + ring.now, c.fb, j, b[j]);
   int T = 0;
   for (; T + 4 <= p.kblocks; T += 4) {
-    k_step<kA, kNB, kTail, 0>(c, lds, acc, a, b, rows, s, next, T);
-    k_step<kA, kNB, kTail, 1>(c, lds, acc, a, b, rows, s, next, T + 1);
-    k_step<kA, kNB, kTail, 2>(c, lds, acc, a, b, rows, s, next, T + 2);
-    k_step<kA, kNB, kTail, 3>(c, lds, acc, a, b, rows, s, next, T + 3);
+    k_step<kA, kNB, kTail, 0>(c, lds, acc, a, b, rows, s, next, ring, T);
+    k_step<kA, kNB, kTail, 1>(c, lds, acc, a, b, rows, s, next, ring, T + 1);
+    k_step<kA, kNB, kTail, 2>(c, lds, acc, a, b, rows, s, next, ring, T + 2);
+    k_step<kA, kNB, kTail, 3>(c, lds, acc, a, b, rows, s, next, ring, T + 3);
   }
-  if (T < p.kblocks) k_step<kA, kNB, kTail, 0>(c, lds, acc, a, b, rows, s, next, T);
-  if (T + 1 < p.kblocks) k_step<kA, kNB, kTail, 1>(c, lds, acc, a, b, rows, s, next, T + 1);
-  if (T + 2 < p.kblocks) k_step<kA, kNB, kTail, 2>(c, lds, acc, a, b, rows, s, next, T + 2);
+  if (T < p.kblocks) k_step<kA, kNB, kTail, 0>(c, lds, acc, a, b, rows, s, next, ring, T);
+  if (T + 1 < p.kblocks) k_step<kA, kNB, kTail, 1>(c, lds, acc, a, b, rows, s, next, ring, T + 1);
+  if (T + 2 < p.kblocks) k_step<kA, kNB, kTail, 2>(c, lds, acc, a, b, rows, s, next, ring, T + 2);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // Register 4 q + t of tile (i, j) holds row 32 i + r, column 32 j + 8 q + 4 h
@@ -387,13 +403,21 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
     uint16_t* to = static_cast<uint16_t*>(p.C) + (int64_t)m_wave * p.N + ncol;
     if (p.N % 8 == 0) {
       const int ch = lane & 15;
-      for (int x0 = 0; x0 < 128; x0 += 4) {
-        const int row = x0 + (lane >> 4);
-        const u32x4_t v =
-            *reinterpret_cast<const u32x4_t*>(park + row * 256 + 16 * (ch ^ (row & 15)));
-        if (m_wave + row < p.M && 8 * ch < cols)
-          __builtin_nontemporal_store(v,
-                                      reinterpret_cast<u32x4_t*>(to + (int64_t)row * p.N + 8 * ch));
+#pragma unroll 1
+      for (int x0 = 0; x0 < 128; x0 += 16) {
+        u32x4_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = x0 + 4 * k + (lane >> 4);
+          v[k] = *reinterpret_cast<const u32x4_t*>(park + row * 256 + 16 * (ch ^ (row & 15)));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = x0 + 4 * k + (lane >> 4);
+          if (m_wave + row < p.M && 8 * ch < cols)
+            __builtin_nontemporal_store(
+                v[k], reinterpret_cast<u32x4_t*>(to + (int64_t)row * p.N + 8 * ch));
+        }
       }
     } else {
       for (int row = 0; row < min(128, p.M - m_wave); ++row)
@@ -411,57 +435,85 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
     // wave's own 16 KiB behind it (128 bytes a row, chunk c at c ^ (row % 8)).
     const int ncol = col0 + 64 * wx;
     uint8_t* own = lds + 2 * kSlot + wave * 16384;
-    for (int part = p.gu ? 0 : 2; part < 3; ++part) {
+    if (p.gu) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int up = 0; up < 2; ++up) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v16f_t g = acc[i][2 * e], u = acc[i][2 * e + 1];
-          asm volatile("" : "+v"(g), "+v"(u));
-          const int row = 32 * i + r;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[4];
+          for (int e = 0; e < 2; ++e) {
+            v16f_t v = acc[i][2 * e + up];
+            asm volatile("" : "+v"(v));
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              v[t] = part == 0 ? g[4 * q + t] : part == 1 ? u[4 * q + t]
-                                                          : silu_f32(g[4 * q + t]) * u[4 * q + t];
-            const uint2 w = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-            uint8_t* at = part < 2 ? own + row * 128 + 16 * ((4 * e + q) ^ (r & 7))
-                                   : lds + (128 * wy + row) * 256 +
-                                         16 * ((8 * wx + 4 * e + q) ^ (r & 15));
-            *reinterpret_cast<uint2*>(at + 8 * h) = w;
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint2*>(own + (32 * i + r) * 128 + 16 * ((4 * e + q) ^ (r & 7)) +
+                                        8 * h) =
+                  make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                             pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+            MXFP4_FENCE();
           }
-          MXFP4_FENCE();
-        }
-      if (part < 2) {
-        uint16_t* to = p.gu + (int64_t)m_wave * 2 * p.N + part * (int64_t)p.N + ncol;
+        uint16_t* to = p.gu + (int64_t)m_wave * 2 * p.N + up * (int64_t)p.N + ncol;
         const int ch = lane & 7;
-        for (int x0 = 0; x0 < 128; x0 += 8) {
-          const int row = x0 + (lane >> 3);
-          const u32x4_t v =
-              *reinterpret_cast<const u32x4_t*>(own + row * 128 + 16 * (ch ^ (row & 7)));
-          if (m_wave + row < p.M)
-            __builtin_nontemporal_store(
-                v, reinterpret_cast<u32x4_t*>(to + (int64_t)row * 2 * p.N + 8 * ch));
+#pragma unroll 1
+        for (int x0 = 0; x0 < 128; x0 += 32) {
+          u32x4_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = x0 + 8 * k + (lane >> 3);
+            v[k] = *reinterpret_cast<const u32x4_t*>(own + row * 128 + 16 * (ch ^ (row & 7)));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = x0 + 8 * k + (lane >> 3);
+            if (m_wave + row < p.M)
+              __builtin_nontemporal_store(
+                  v[k], reinterpret_cast<u32x4_t*>(to + (int64_t)row * 2 * p.N + 8 * ch));
+          }
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v16f_t g = acc[i][2 * e], u = acc[i][2 * e + 1];
+        asm volatile("" : "+v"(g), "+v"(u));
+        const int row = 32 * i + r;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = silu_f32(g[4 * q + t]) * u[4 * q + t];
+          *reinterpret_cast<uint2*>(lds + (128 * wy + row) * 256 +
+                                    16 * ((8 * wx + 4 * e + q) ^ (r & 15)) + 8 * h) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+        MXFP4_FENCE();
+      }
     __syncthreads();
     // The quantize of a row's 128 activations: 16 lanes, as quantize_fp8.hip.
     const int ch = lane & 15;
     uint16_t* act_bf16 = static_cast<uint16_t*>(p.C);
-    for (int x0 = 0; x0 < 64; x0 += 4) {
-      const int row = 64 * wave + x0 + (lane >> 4), m = row0 + row;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds + row * 256 + 16 * (ch ^ (row & 15)));
-      const uint32_t byte = fp8_row_scale<kE4M3>(v);
-      const uint2 code = fp8_encode_chunk<kE4M3>(v, fp8_scale_value(byte));
-      if (m < p.M) {
-        *reinterpret_cast<uint2*>(act.codes + (int64_t)m * p.N + col0 + 8 * ch) = code;
-        if (ch == 0) act.scales[(int64_t)m * (p.N / kFp8Block) + tn] = (uint8_t)byte;
-        if (act_bf16)
-          __builtin_nontemporal_store(
-              v, reinterpret_cast<u32x4_t*>(act_bf16 + (int64_t)m * p.N + col0 + 8 * ch));
+#pragma unroll 1
+    for (int x0 = 0; x0 < 64; x0 += 16) {
+      u32x4_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 64 * wave + x0 + 4 * k + (lane >> 4);
+        v[k] = *reinterpret_cast<const u32x4_t*>(lds + row * 256 + 16 * (ch ^ (row & 15)));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int m = row0 + 64 * wave + x0 + 4 * k + (lane >> 4);
+        const uint32_t byte = fp8_row_scale<kE4M3>(v[k]);
+        const uint2 code = fp8_encode_chunk<kE4M3>(v[k], fp8_scale_value(byte));
+        if (m < p.M) {
+          *reinterpret_cast<uint2*>(act.codes + (int64_t)m * p.N + col0 + 8 * ch) = code;
+          if (ch == 0) act.scales[(int64_t)m * (p.N / kFp8Block) + tn] = (uint8_t)byte;
+          if (act_bf16)
+            __builtin_nontemporal_store(
+                v[k], reinterpret_cast<u32x4_t*>(act_bf16 + (int64_t)m * p.N + col0 + 8 * ch));
+        }
       }
     }
   }

@@ -16,16 +16,17 @@
 // once) into two slots of A and three of B (160 KiB), in rows of eight 16-byte
 // chunks XOR-swizzled by the row, so that fragment reads fall on all banks.
 //
-// Schedule of a step. A slice runs in two halves, B tiles 0 and 1 with all four
-// of A, then 2 and 3, so that every fragment has one set of registers (64) and
-// is read for the next use while the other half runs: B's two of the half just
-// done at once, A's one by one behind their last use. All reads of a step are
-// done after the first half of its second slice; there the waves meet (the next
-// step's tiles have landed, this step's may be overwritten), and the DMAs of the
-// step after next go out over the next 16 instructions: A's a whole step ahead,
-// B's, which have a third slot, nearly two.
+// Schedule of a step. The fragments of a slice have two sets of registers: the 16
+// reads of the next slice go out beside the first instructions of this one, a
+// slice ahead of their use (with one set, read behind the last use, a fifth of
+// the time went into waiting for LDS reads). Between the two slices of a step
+// the waves meet: the step has been read, the next one's tiles have landed, and
+// the DMAs of the step after next go out beside the instructions, A's a whole
+// step ahead, B's, which have a third slot, one and a half.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "fp8.h"
 
@@ -47,6 +48,7 @@ struct Ctx {
   uint32_t lds;                 // of this wave's rows in slot 0 of A
   uint32_t fa[4], fb[4];        // fragment reads of quarter q of a step, slot 0
   int last;                     // last K step
+  int rot;                      // the K step this tile begins with
   int tail_bytes;               // of the last step, where K % 128 != 0
   int chunk[2];                 // the chunk a lane fetches, rows at 0 and 8 mod 16
 };
@@ -89,40 +91,60 @@ __device__ __forceinline__ void load_pair(const Ctx& c, int kb, uint32_t slot) {
   }
 }
 
-// 32 codes of one row: half a 64-wide slice of K.
+// The K step loaded as step t (a tile's steps go around from rot); past the
+// last it is loaded again, and not used.
+__device__ __forceinline__ int phys_step(const Ctx& c, int t) {
+  const int k = min(t, c.last) + c.rot;
+  return k > c.last ? k - c.last - 1 : k;
+}
+
+// 32 codes of one row, half a 64-wide slice of K; and a wave's fragments of one
+// slice.
 struct Frag {
-  u32x4_t lo, hi;
+  u32x4_t half[2];
+};
+struct Frags {
+  Frag a[4], b[4];
 };
 
-template <int kSlice>
-__device__ __forceinline__ void read_frag(const uint8_t* lds, const uint32_t (&at)[4], int tile,
-                                          Frag& f) {
-  const uint8_t* p = lds + tile * 32 * kRowBytes;
-  f.lo = *reinterpret_cast<const u32x4_t*>(p + at[2 * kSlice]);
-  f.hi = *reinterpret_cast<const u32x4_t*>(p + at[2 * kSlice + 1]);
+// Read kRead (0 .. 15) of the fragments of a slice: B's eight halves, then A's.
+template <int kSlice, int kRead>
+__device__ __forceinline__ void read_half(const Ctx& c, const uint8_t* lds_a, const uint8_t* lds_b,
+                                          Frags& f) {
+  constexpr int kTileOf = (kRead & 7) >> 1, kHalf = kRead & 1;
+  const uint8_t* p = (kRead < 8 ? lds_b + c.fb[2 * kSlice + kHalf]
+                                : lds_a + c.fa[2 * kSlice + kHalf]) + kTileOf * 32 * kRowBytes;
+  (kRead < 8 ? f.b[kTileOf] : f.a[kTileOf]).half[kHalf] = *reinterpret_cast<const u32x4_t*>(p);
+}
+
+template <int... kReads>
+__device__ __forceinline__ void read_all(const Ctx& c, const uint8_t* lds_a, const uint8_t* lds_b,
+                                         Frags& f, std::integer_sequence<int, kReads...>) {
+  (read_half<0, kReads>(c, lds_a, lds_b, f), ...);
 }
 
 template <Fp8Type kA>
 __device__ __forceinline__ void mma(v16f_t& acc, const Frag& x, const Frag& y, uint32_t sx,
                                     uint32_t sy) {
-  const v8i_t xv = {(int)x.lo[0], (int)x.lo[1], (int)x.lo[2], (int)x.lo[3],
-                    (int)x.hi[0], (int)x.hi[1], (int)x.hi[2], (int)x.hi[3]};
-  const v8i_t yv = {(int)y.lo[0], (int)y.lo[1], (int)y.lo[2], (int)y.lo[3],
-                    (int)y.hi[0], (int)y.hi[1], (int)y.hi[2], (int)y.hi[3]};
+  const u32x4_t x0 = x.half[0], x1 = x.half[1], y0 = y.half[0], y1 = y.half[1];
+  const v8i_t xv = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3],
+                    (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+  const v8i_t yv = {(int)y0[0], (int)y0[1], (int)y0[2], (int)y0[3],
+                    (int)y1[0], (int)y1[1], (int)y1[2], (int)y1[3]};
   acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xv, yv, acc, kE4M3, kA, 0, (int)sx, 0,
                                                         (int)sy);
 }
 
 #define MXFP4_FENCE() __builtin_amdgcn_sched_barrier(0)
 
-// End of a group of two matrix instructions with kReads LDS reads beside them:
-// half of the reads after each.
-template <int kReads>
+// End of a group of two matrix instructions: so many LDS reads after the first
+// and after the second.
+template <int kFirst, int kSecond>
 __device__ __forceinline__ void group_end() {
   __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-  if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads / 2, 0);
+  if constexpr (kFirst > 0) __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
   __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-  if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads / 2, 0);
+  if constexpr (kSecond > 0) __builtin_amdgcn_sched_group_barrier(0x100, kSecond, 0);
   MXFP4_FENCE();
 }
 
@@ -153,108 +175,80 @@ struct Ring {
   uint32_t now, next, free;
 };
 
-// One K step T, P = T % 4, A in slot P % 2. Fragments of its first slice are
-// there but for A's tile 3.
+// The 16 matrix instructions of one slice on fragments f, with the 16 reads of
+// the next slice (kSlice of the step in lds_a, lds_b) into g and the four pairs
+// of DMAs of operand kOp for step k into `slot`. The reads come early, so that
+// they have returned when the slice ends.
+template <Fp8Type kA, int kNB, bool kTail, int kSlice, int kOp>
+__device__ __forceinline__ void slice(const Ctx& c, v16f_t (&acc)[4][4], const Frags& f, Frags& g,
+                                      const uint8_t* lds_a, const uint8_t* lds_b,
+                                      const Scales<kNB>& s, int k, uint32_t slot) {
+  const auto sb = [&](int j) { return s.b[kNB == 1 ? 0 : kNB == 2 ? j & 1 : j]; };
+#define MXFP4_MMA2(i, j)                                           \
+  mma<kA>(acc[i][j], f.b[j], f.a[i], sb(j), s.a[i]);               \
+  mma<kA>(acc[i][(j) + 1], f.b[(j) + 1], f.a[i], sb((j) + 1), s.a[i])
+#define MXFP4_READ(n) read_half<kSlice, n>(c, lds_a, lds_b, g)
+  MXFP4_MMA2(0, 0);
+  MXFP4_READ(0);
+  MXFP4_READ(1);
+  MXFP4_READ(2);
+  load_pair<kOp, 0, kTail>(c, k, slot);
+  group_end<2, 1>();
+  MXFP4_MMA2(0, 2);
+  MXFP4_READ(3);
+  MXFP4_READ(4);
+  MXFP4_READ(5);
+  group_end<2, 1>();
+  MXFP4_MMA2(1, 0);
+  MXFP4_READ(6);
+  MXFP4_READ(7);
+  MXFP4_READ(8);
+  load_pair<kOp, 2, kTail>(c, k, slot);
+  group_end<2, 1>();
+  MXFP4_MMA2(1, 2);
+  MXFP4_READ(9);
+  MXFP4_READ(10);
+  MXFP4_READ(11);
+  group_end<2, 1>();
+  MXFP4_MMA2(2, 0);
+  MXFP4_READ(12);
+  MXFP4_READ(13);
+  load_pair<kOp, 4, kTail>(c, k, slot);
+  group_end<1, 1>();
+  MXFP4_MMA2(2, 2);
+  MXFP4_READ(14);
+  MXFP4_READ(15);
+  group_end<1, 1>();
+  MXFP4_MMA2(3, 0);
+  load_pair<kOp, 6, kTail>(c, k, slot);
+  group_end<0, 0>();
+  MXFP4_MMA2(3, 2);
+  group_end<0, 0>();
+#undef MXFP4_MMA2
+#undef MXFP4_READ
+}
+
+// One K step T, P = T % 4, A in slot P % 2: f holds its first slice.
 template <Fp8Type kA, int kNB, bool kTail, int P>
 __device__ __forceinline__ void k_step(const Ctx& c, const uint8_t* lds, v16f_t (&acc)[4][4],
-                                       Frag (&a)[4], Frag (&b)[4], const ScaleRows<kNB>& rows,
+                                       Frags& f, Frags& g, const ScaleRows<kNB>& rows,
                                        Scales<kNB>& s, Scales<kNB>& next, Ring& ring, int T) {
-  constexpr int S = P & 1;
-  const uint8_t* lds_a = lds + S * kSlot;
-  const uint8_t* lds_a1 = lds + (1 - S) * kSlot;
-  const uint8_t* lds_b = lds + ring.now;
-  const uint8_t* lds_b1 = lds + ring.next;
-  const int k2 = min(T + 2, c.last);
-  const auto sb = [&](int j) { return s.b[kNB == 1 ? 0 : kNB == 2 ? j & 1 : j]; };
-#define MXFP4_MMA(i, j) mma<kA>(acc[i][j], b[j], a[i], sb(j), s.a[i])
-  // Slice 0, B tiles 0, 1; the DMAs of step T + 2's B.
-  MXFP4_MMA(0, 0);
-  MXFP4_MMA(0, 1);
-  read_frag<0>(lds_a, c.fa, 3, a[3]);
-  load_pair<1, 0, kTail>(c, k2, ring.free);
-  group_end<2>();
-  MXFP4_MMA(1, 0);
-  MXFP4_MMA(1, 1);
-  read_frag<0>(lds_b, c.fb, 2, b[2]);
-  load_pair<1, 2, kTail>(c, k2, ring.free);
-  group_end<2>();
-  MXFP4_MMA(2, 0);
-  MXFP4_MMA(2, 1);
-  read_frag<0>(lds_b, c.fb, 3, b[3]);
-  load_pair<1, 4, kTail>(c, k2, ring.free);
-  group_end<2>();
-  MXFP4_MMA(3, 0);
-  MXFP4_MMA(3, 1);
-  load_pair<1, 6, kTail>(c, k2, ring.free);
-  group_end<0>();
-  // B tiles 2, 3.
-  MXFP4_MMA(0, 2);
-  MXFP4_MMA(0, 3);
-  read_frag<1>(lds_b, c.fb, 0, b[0]);
-  group_end<2>();
-  MXFP4_MMA(1, 2);
-  MXFP4_MMA(1, 3);
-  read_frag<1>(lds_b, c.fb, 1, b[1]);
-  read_frag<1>(lds_a, c.fa, 0, a[0]);
-  group_end<4>();
-  MXFP4_MMA(2, 2);
-  MXFP4_MMA(2, 3);
-  read_frag<1>(lds_a, c.fa, 1, a[1]);
-  group_end<2>();
-  MXFP4_MMA(3, 2);
-  MXFP4_MMA(3, 3);
-  read_frag<1>(lds_a, c.fa, 2, a[2]);
-  group_end<2>();
-  // Slice 1.
-  MXFP4_MMA(0, 0);
-  MXFP4_MMA(0, 1);
-  read_frag<1>(lds_a, c.fa, 3, a[3]);
-  group_end<2>();
-  MXFP4_MMA(1, 0);
-  MXFP4_MMA(1, 1);
-  read_frag<1>(lds_b, c.fb, 2, b[2]);
-  group_end<2>();
-  MXFP4_MMA(2, 0);
-  MXFP4_MMA(2, 1);
-  read_frag<1>(lds_b, c.fb, 3, b[3]);
-  group_end<2>();
-  MXFP4_MMA(3, 0);
-  MXFP4_MMA(3, 1);
-  group_end<0>();
-  // All but the last 8 loads (step T + 2's B): step T + 1 has landed.
+  constexpr uint32_t kSlotA = (P & 1) * kSlot;
+  const int k2 = phys_step(c, T + 2);
+  slice<kA, kNB, kTail, 1, 1>(c, acc, f, g, lds + kSlotA, lds + ring.now, s, k2, ring.free);
+  // All but the last 8 loads (step T + 2's B): step T + 1 has landed; and this
+  // step has been read.
   asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   MXFP4_FENCE();
   if constexpr (P == 3) {
-    // The next words were loaded in the step before: landed by now.
+    // The next words were loaded two steps before: landed by now.
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(next.a[i]));
 #pragma unroll
     for (int j = 0; j < kNB; ++j) asm volatile("" : "+v"(next.b[j]));
   }
-  if constexpr (P == 1) load_scales(rows, T + 3, next);  // past the last: not used
-  // B tiles 2, 3; the first fragments of step T + 1, the DMAs of step T + 2's A.
-  MXFP4_MMA(0, 2);
-  MXFP4_MMA(0, 3);
-  read_frag<0>(lds_b1, c.fb, 0, b[0]);
-  load_pair<0, 0, kTail>(c, k2, S * kSlot);
-  group_end<2>();
-  MXFP4_MMA(1, 2);
-  MXFP4_MMA(1, 3);
-  read_frag<0>(lds_b1, c.fb, 1, b[1]);
-  read_frag<0>(lds_a1, c.fa, 0, a[0]);
-  load_pair<0, 2, kTail>(c, k2, S * kSlot);
-  group_end<4>();
-  MXFP4_MMA(2, 2);
-  MXFP4_MMA(2, 3);
-  read_frag<0>(lds_a1, c.fa, 1, a[1]);
-  load_pair<0, 4, kTail>(c, k2, S * kSlot);
-  group_end<2>();
-  MXFP4_MMA(3, 2);
-  MXFP4_MMA(3, 3);
-  read_frag<0>(lds_a1, c.fa, 2, a[2]);
-  load_pair<0, 6, kTail>(c, k2, S * kSlot);
-  group_end<2>();
-#undef MXFP4_MMA
+  if constexpr (P == 1) load_scales(rows, phys_step(c, T + 3), next);
+  slice<kA, kNB, kTail, 0, 0>(c, acc, g, f, lds + (kSlot - kSlotA), lds + ring.next, s, k2, kSlotA);
   ring = Ring{ring.next, ring.free, ring.now};
   if constexpr (P == 3) {
     s = next;
@@ -297,6 +291,13 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
 
   Ctx c;
   c.last = p.kblocks - 1;
+  // XCD x starts x / 8 into K, and every other tile of its neighbourhood 4 steps
+  // further on, so that the tiles that share rows of an operand do not all wait
+  // for the same lines (16384 x 28672 x 4096 1475 -> 1456 us). Where the scales
+  // of K are not whole words, steps begin at 0.
+  c.rot = kTail || p.kblocks % 4 != 0
+              ? 0
+              : (4 * ((id % 8) * (p.kblocks / 4) / 8) + 4 * ((tm + tn) & 1)) % p.kblocks;
   c.tail_bytes = p.K - c.last * kFp8Block;
   c.lds = lds_addr(lds) + wave * 8192;
   const int64_t a_first = min(row0 + 64 * wave, p.M - 1);
@@ -334,18 +335,18 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
     rows.b[j] = (b_row(128 * wx + 32 * j + (kRowsB ? r : 0)) >> p.b_shift) * p.kblocks;
 
   Scales<kNB> s, next;
-  load_scales(rows, 0, s);
+  load_scales(rows, c.rot, s);
   next = s;
   Ring ring{2 * kSlot, 3 * kSlot, 4 * kSlot};
-  const int k1 = min(1, c.last);
-  load_pair<0, 0, kTail>(c, 0, 0);
-  load_pair<0, 2, kTail>(c, 0, 0);
-  load_pair<0, 4, kTail>(c, 0, 0);
-  load_pair<0, 6, kTail>(c, 0, 0);
-  load_pair<1, 0, kTail>(c, 0, ring.now);
-  load_pair<1, 2, kTail>(c, 0, ring.now);
-  load_pair<1, 4, kTail>(c, 0, ring.now);
-  load_pair<1, 6, kTail>(c, 0, ring.now);
+  const int k0 = c.rot, k1 = phys_step(c, 1);
+  load_pair<0, 0, kTail>(c, k0, 0);
+  load_pair<0, 2, kTail>(c, k0, 0);
+  load_pair<0, 4, kTail>(c, k0, 0);
+  load_pair<0, 6, kTail>(c, k0, 0);
+  load_pair<1, 0, kTail>(c, k0, ring.now);
+  load_pair<1, 2, kTail>(c, k0, ring.now);
+  load_pair<1, 4, kTail>(c, k0, ring.now);
+  load_pair<1, 6, kTail>(c, k0, ring.now);
   load_pair<1, 0, kTail>(c, k1, ring.next);
   load_pair<1, 2, kTail>(c, k1, ring.next);
   load_pair<1, 4, kTail>(c, k1, ring.next);
@@ -361,21 +362,18 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
     for (int j = 0; j < 4; ++j) acc[i][j] = v16f_t{};
   // Step 0 has landed; the 16 DMAs of step 1 may be under way.
   asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
-  Frag a[4], b[4];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) read_frag<0>(lds, c.fa, i, a[i]);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) read_frag<0>(lds + ring.now, c.fb, j, b[j]);
+  Frags f, g;
+  read_all(c, lds, lds + ring.now, f, std::make_integer_sequence<int, 16>());
   int T = 0;
   for (; T + 4 <= p.kblocks; T += 4) {
-    k_step<kA, kNB, kTail, 0>(c, lds, acc, a, b, rows, s, next, ring, T);
-    k_step<kA, kNB, kTail, 1>(c, lds, acc, a, b, rows, s, next, ring, T + 1);
-    k_step<kA, kNB, kTail, 2>(c, lds, acc, a, b, rows, s, next, ring, T + 2);
-    k_step<kA, kNB, kTail, 3>(c, lds, acc, a, b, rows, s, next, ring, T + 3);
+    k_step<kA, kNB, kTail, 0>(c, lds, acc, f, g, rows, s, next, ring, T);
+    k_step<kA, kNB, kTail, 1>(c, lds, acc, f, g, rows, s, next, ring, T + 1);
+    k_step<kA, kNB, kTail, 2>(c, lds, acc, f, g, rows, s, next, ring, T + 2);
+    k_step<kA, kNB, kTail, 3>(c, lds, acc, f, g, rows, s, next, ring, T + 3);
   }
-  if (T < p.kblocks) k_step<kA, kNB, kTail, 0>(c, lds, acc, a, b, rows, s, next, ring, T);
-  if (T + 1 < p.kblocks) k_step<kA, kNB, kTail, 1>(c, lds, acc, a, b, rows, s, next, ring, T + 1);
-  if (T + 2 < p.kblocks) k_step<kA, kNB, kTail, 2>(c, lds, acc, a, b, rows, s, next, ring, T + 2);
+  if (T < p.kblocks) k_step<kA, kNB, kTail, 0>(c, lds, acc, f, g, rows, s, next, ring, T);
+  if (T + 1 < p.kblocks) k_step<kA, kNB, kTail, 1>(c, lds, acc, f, g, rows, s, next, ring, T + 1);
+  if (T + 2 < p.kblocks) k_step<kA, kNB, kTail, 2>(c, lds, acc, f, g, rows, s, next, ring, T + 2);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // Register 4 q + t of tile (i, j) holds row 32 i + r, column 32 j + 8 q + 4 h

@@ -230,6 +230,11 @@ struct Fp8GemmArgs {
   uint16_t* gu;   // with glu: g and u, BF16 [M, 2 I], or null
 };
 enum Fp8Out { kFp8Bf16 = 0, kFp8F32 = 1, kFp8Glu = 2 };
+// Whether either operand has fewer than four bytes of UE8M0 scales (the kernels
+// read four at a time; launch_gemm_fp8_small takes these products too).
+inline bool fp8_short_scales(int64_t M, int64_t N, int64_t kblocks, int b_shift) {
+  return M * kblocks < 4 || ((N + (int64_t(1) << b_shift) - 1) >> b_shift) * kblocks < 4;
+}
 hipError_t launch_gemm_fp8_small(const Fp8GemmArgs& a, Fp8Out out, Fp8Type a_type, bool scale_f32,
                                  hipStream_t stream);
 

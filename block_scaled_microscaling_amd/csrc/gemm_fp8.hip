@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
         b[i] = static_cast<const uint32_t*>(p.Bs)[sb_at[i] + kb];
       } else {
         a[i] = scale_word(static_cast<const uint8_t*>(p.As), sa_at[i] + kb, sa_total);
-        b[i] = short_scale_word(static_cast<const uint8_t*>(p.Bs), sb_at[i] + kb, sb_total);
+        b[i] = scale_word(static_cast<const uint8_t*>(p.Bs), sb_at[i] + kb, sb_total);
       }
     }
   };
@@ -365,28 +365,27 @@ hipError_t launch_typed(const Fp8GemmArgs& a, Fp8Out out, bool f32, hipStream_t 
              : launch<false, false, kFp8Bf16, kA>(a, stream);
 }
 
-constexpr int kSmallMaxM = 64;
+constexpr int kSmallMaxM = 512;
 
-// Whether a product runs on 256 x 256 tiles: where they fill the chip. (B's
-// scales are then read four bytes at a time.)
-bool big_tiles(int64_t M, int64_t N, int64_t K) {
-  return M > 256 && ((M + 255) / 256) * ((N + 255) / 256) > 128 &&
-         (N + 127) / 128 * ((K + 127) / 128) >= 4;
+// Whether a product runs on 256 x 256 tiles: where they fill the chip.
+bool big_tiles(int64_t M, int64_t N) {
+  return M > 256 && ((M + 255) / 256) * ((N + 255) / 256) > 128;
 }
 
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& a, Fp8Out out, Fp8Type a_type, bool scale_f32,
                            hipStream_t stream) {
-  if (a.M <= kSmallMaxM) return launch_gemm_fp8_small(a, out, a_type, scale_f32, stream);
-  if (out == kFp8Bf16 && !scale_f32 && big_tiles(a.M, a.N, a.K))
+  if (a.M <= kSmallMaxM || (!scale_f32 && fp8_short_scales(a.M, a.N, a.kblocks, a.b_shift)))
+    return launch_gemm_fp8_small(a, out, a_type, scale_f32, stream);
+  if (out == kFp8Bf16 && !scale_f32 && big_tiles(a.M, a.N))
     return launch_gemm_fp8_tile(a, out, a_type, Fp8ActOut{}, stream);
   return a_type == kE4M3 ? launch_typed<kE4M3>(a, out, scale_f32, stream)
                          : launch_typed<kE5M2>(a, out, scale_f32, stream);
 }
 
 bool gemm_fp8_swiglu_small(int64_t M, int64_t I, int64_t K) {
-  return !big_tiles(M, 2 * I, K);
+  return !big_tiles(M, 2 * I) || fp8_short_scales(M, 2 * I, (K + kFp8Block - 1) / kFp8Block, 7);
 }
 
 hipError_t launch_gemm_fp8_swiglu(const Fp8GemmArgs& a, uint8_t* codes, uint8_t* scales,
@@ -395,7 +394,7 @@ hipError_t launch_gemm_fp8_swiglu(const Fp8GemmArgs& a, uint8_t* codes, uint8_t*
     return launch_gemm_fp8_tile(a, kFp8Glu, kE4M3, Fp8ActOut{codes, scales}, stream);
   Fp8GemmArgs g = a;
   if (!g.C) g.C = workspace;
-  const hipError_t e = a.M <= kSmallMaxM
+  const hipError_t e = a.M <= kSmallMaxM || fp8_short_scales(a.M, 2 * (int64_t)a.N, a.kblocks, 7)
                            ? launch_gemm_fp8_small(g, kFp8Glu, kE4M3, false, stream)
                            : launch<false, false, kFp8Glu, kE4M3>(g, stream);
   if (e != hipSuccess) return e;

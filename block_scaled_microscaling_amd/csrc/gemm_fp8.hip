@@ -1,28 +1,36 @@
-// FP8 GEMM on 128 x 128 tiles: C[m, n] = sum over blocks kb of 128 of
-// sa[m, kb] sb[n, kb] sum_k a[m, k] b[n, k], in BF16 or FP32, or the gate+up
-// product of a gated MLP with act = silu(g) u in BF16; and the choice of the
-// kernel for every FP8 product.
+// FP8 GEMM on tiles of 128 x 128 or 128 x 256: C[m, n] = sum over blocks kb of
+// 128 of sa[m, kb] sb[n, kb] sum_k a[m, k] b[n, k], in BF16 or FP32, or the
+// gate+up product of a gated MLP with act = silu(g) u in BF16; and the choice of
+// the kernel for every FP8 product.
 //
-// Tiling. A workgroup of 4 waves owns a 128 x 128 tile of C, wave (wy, wx) a 64
-// x 64 part: 2 x 2 tiles of the 32 x 32 matrix instructions, B's fragment the
-// first operand, so that a lane ends with four consecutive columns of one row.
-// Two workgroups share a CU (64 KiB of LDS each), one computing while the
-// other waits.
+// Tiling. One workgroup of 4 waves (one per SIMD) owns a tile of C, wave (wy, wx)
+// 64 rows and 32 kNT columns of it: 2 x kNT tiles of the 32 x 32 matrix
+// instructions, B's fragment the first operand, so that a lane ends with four
+// consecutive columns of one row. With at most 128 accumulators a lane the
+// vector registers hold them, which FP32 scales need: a block's sums times its
+// scale are added on the VALU (on 256 x 256 tiles they would go to and from the
+// accumulation registers, three instructions for one).
 //
-// Data movement. A K step is one block: 128 bytes a row, a whole line. Tiles go
-// global -> LDS by DMA, 8 rows an instruction, one step ahead, in rows of eight
-// 16-byte chunks XOR-swizzled by the row, so that a fragment's reads fall on
-// all banks. Rows past M or N re-read the last one; chunks past K in a last
-// step that is short come from a line of zeros (kTail).
+// Data movement. A K step is one block: 128 bytes a row, a whole line. Tiles and
+// scales (one dword a row) go global -> LDS by DMA into a ring of kSlots slots,
+// tiles in rows of eight 16-byte chunks XOR-swizzled by the row, so that a
+// fragment's reads fall on all banks. The fragments of a step are read while the
+// step before is multiplied, so a slot is free once its step begins, and loads
+// run kSlots steps ahead. Every wave issues the same number of DMAs a step, and
+// nothing else that counts with them; so a wait names how many may be under way.
+// Rows past M or N re-read the last one; chunks past K in a last step that is
+// short come from a line of zeros (kTail).
 //
 // Arithmetic (fp8.h says why there are two):
 //   FP8 codes straight into v_mfma_scale_f32_32x32x64_f8f6f4, or converted to
 //   BF16 and through v_mfma_f32_32x32x16_bf16. UE8M0 scales go into the first
 //   and into the conversion of the second; FP32 scales multiply each block's
-//   sums (a lane holds one row of A, and B's scale is the wave's own), which
-//   costs one FMA an element and block.
+//   sums (a lane holds one row of A, and B's scale is the wave's own).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
+#include <utility>
 
 #include "fp8.h"
 
@@ -30,20 +38,36 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;                    // rows of A and of B per workgroup
-constexpr int kRowBytes = kFp8Block;          // of one row in a K step
-constexpr int kSlotBytes = kTile * kRowBytes;  // 16 KiB an operand
+constexpr int kRows = 128;            // of A per workgroup
+constexpr int kRowBytes = kFp8Block;  // of one row in a K step
 constexpr int kGroupM = 8;
+
+// Columns of a tile, its LDS slot and ring, and the DMAs of a wave's step: 4 of
+// A's rows, 2 kNT of B's, and 64 rows of scales (two of them with kNT = 4).
+template <int kNT>
+struct Geom {
+  static constexpr int kCols = 64 * kNT;
+  static constexpr int kTiles = (kRows + kCols) * kRowBytes;
+  static constexpr int kScaleDmas = kNT / 2;
+  static constexpr int kSlot = kTiles + (kRows + kCols) * 4;
+  static constexpr int kSlots = kNT == 2 ? 4 : 3;
+  static constexpr int kDmas = 4 + 2 * kNT + kScaleDmas;
+};
 
 typedef float v16_t __attribute__((ext_vector_type(16)));
 
 // One block of K: codes of a 32-row tile, chunks h, 2 + h, 4 + h, 6 + h of the
-// lane's row.
+// lane's row; and all of a wave's, with their scales.
 struct Frag {
   u32x4_t c[4];
 };
+template <int kNT>
+struct Frags {
+  Frag a[2], b[kNT];
+  uint32_t sa[2], sb[kNT];
+};
 
-template <Fp8Type kA, int kScaleOp>
+template <Fp8Type kA>
 __device__ __forceinline__ v16_t mfma_fp8_32(const Frag& x, const Frag& y, int s, v16_t c,
                                              uint32_t sx, uint32_t sy) {
   const u32x4_t x0 = x.c[2 * s], x1 = x.c[2 * s + 1], y0 = y.c[2 * s], y1 = y.c[2 * s + 1];
@@ -51,15 +75,111 @@ __device__ __forceinline__ v16_t mfma_fp8_32(const Frag& x, const Frag& y, int s
                     (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
   const v8i_t yv = {(int)y0[0], (int)y0[1], (int)y0[2], (int)y0[3],
                     (int)y1[0], (int)y1[1], (int)y1[2], (int)y1[3]};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xv, yv, c, kE4M3, kA, kScaleOp, (int)sx,
-                                                         kScaleOp, (int)sy);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xv, yv, c, kE4M3, kA, 0, (int)sx, 0,
+                                                         (int)sy);
 }
 
-template <bool kBf16, bool kF32Scale, Fp8Out kOut, Fp8Type kA, bool kTail>
-__global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, int tiles_m,
-                                                               int tiles_n) {
+// Pieces that a step's products come in, each with a share of the next step's
+// reads and of the DMAs beside it.
+template <int kNT, bool kBf16>
+constexpr int kPiecesOf = kBf16 ? 8 : 2 * kNT;
+template <int n>
+using Int = std::integral_constant<int, n>;
+template <class F, int... n>
+__device__ __forceinline__ void for_each(F f, std::integer_sequence<int, n...>) {
+  (f(Int<n>()), ...);
+}
+
+// acc += the products of one step; beside(Int<n>) goes out with piece n. Without
+// that order, kept by fences, the compiler moved the reads behind the matrix
+// instructions and then waited for them (512 x 8192 x 8192 47 us).
+template <bool kBf16, bool kF32Scale, Fp8Type kA, int kNT, class Beside>
+__device__ __forceinline__ void multiply(v16_t (&acc)[2][kNT], const Frags<kNT>& f,
+                                         Beside beside) {
+  const auto pieces = std::make_integer_sequence<int, kPiecesOf<kNT, kBf16>>();
+  if constexpr (kBf16) {
+    v16_t sums[2][kNT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) sums[i][j] = kF32Scale ? v16_t{} : acc[i][j];
+    for_each([&](auto n) {
+      constexpr int c = n() / 2, e = n() % 2;
+      bf16x8_t a[2], b[kNT];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        a[i] = fp8x8_to_bf16<kA>(f.a[i].c[c][2 * e], f.a[i].c[c][2 * e + 1],
+                                 kF32Scale ? 1.0f : fp8_scale_value(f.sa[i]));
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+        b[j] = fp8x8_to_bf16<kE4M3>(f.b[j].c[c][2 * e], f.b[j].c[c][2 * e + 1],
+                                    kF32Scale ? 1.0f : fp8_scale_value(f.sb[j]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+          sums[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], sums[i][j], 0, 0, 0);
+      beside(n);
+      __builtin_amdgcn_sched_barrier(0);
+    }, pieces);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) {
+        if constexpr (kF32Scale) {
+          const float scale = __uint_as_float(f.sa[i]) * __uint_as_float(f.sb[j]);
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(scale, sums[i][j][v], acc[i][j][v]);
+        } else {
+          acc[i][j] = sums[i][j];
+        }
+      }
+  } else if constexpr (kF32Scale) {
+    // A tile's sums are added while the next one's are made.
+    v16_t sums[2];
+    const auto add = [&](int t) {
+      const float scale = __uint_as_float(f.sa[t / kNT]) * __uint_as_float(f.sb[t % kNT]);
+      v16_t& to = acc[t / kNT][t % kNT];
+#pragma unroll
+      for (int v = 0; v < 16; ++v) to[v] = fmaf(scale, sums[t & 1][v], to[v]);
+    };
+    for_each([&](auto n) {
+      constexpr int i = n() / kNT, j = n() % kNT;
+      v16_t d = mfma_fp8_32<kA>(f.b[j], f.a[i], 0, v16_t{}, 127, 127);
+      sums[n() & 1] = mfma_fp8_32<kA>(f.b[j], f.a[i], 1, d, 127, 127);
+      if constexpr (n() > 0) add(n() - 1);
+      beside(n);
+      __builtin_amdgcn_sched_barrier(0);
+    }, pieces);
+    add(2 * kNT - 1);
+  } else {
+    for_each([&](auto n) {
+      constexpr int i = n() / kNT, j = n() % kNT;
+      acc[i][j] = mfma_fp8_32<kA>(f.b[j], f.a[i], 0, acc[i][j], f.sb[j], f.sa[i]);
+      acc[i][j] = mfma_fp8_32<kA>(f.b[j], f.a[i], 1, acc[i][j], f.sb[j], f.sa[i]);
+      beside(n);
+      __builtin_amdgcn_sched_barrier(0);
+    }, pieces);
+  }
+}
+
+// A byte per lane, into the lane's dword of LDS.
+__device__ __forceinline__ void dma1(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off"
+               :: "v"(g), "s"(lds) : "m0");
+}
+
+template <int kLeft>
+__device__ __forceinline__ void wait_loads_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(kLeft) : "memory");
+}
+
+template <int kNT, bool kBf16, bool kF32Scale, Fp8Out kOut, Fp8Type kA, bool kTail>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_fp8_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n) {
   constexpr bool kGlu = kOut == kFp8Glu;
-  __shared__ __align__(16) uint8_t lds[4 * kSlotBytes];  // slots 0, 1 of A, then of B
+  using G = Geom<kNT>;
+  __shared__ __align__(16) uint8_t lds[G::kSlots * G::kSlot];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -69,11 +189,12 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
   if (id < 0) return;
   int tm, tn;
   xcd_tile(id, tiles_m, tiles_n, kGroupM, tm, tn);
-  const int row0 = tm * kTile;
-  const int col0 = tn * (kGlu ? kTile / 2 : kTile);
+  const int row0 = tm * kRows;
+  const int col0 = tn * (kGlu ? G::kCols / 2 : G::kCols);
 
   // B's row of tile row t. kGlu: a tile is 64 columns of act, wave column wx has
   // 32 of them, its first tile their gate rows, its second their up rows.
+  static_assert(!kGlu || kNT == 2);
   const auto b_row = [&](int t) -> int64_t {
     if constexpr (kGlu)
       return (int64_t)min(col0 + 32 * (t >> 6) + (t & 31), p.N - 1) + ((t >> 5) & 1) * (int64_t)p.N;
@@ -81,176 +202,133 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
       return min(col0 + t, p.N - 1);
   };
 
-  // This wave's DMAs: tile rows 32 w + 8 q + lane / 8 of each operand; lane l
-  // lands at chunk l % 8 of its row and so fetches chunk (l % 8) ^ swizzle.
+  // This wave's DMAs: tile rows 32 w + 8 q + lane / 8 of A, 16 kNT w + 8 q + lane
+  // / 8 of B; lane l lands at chunk l % 8 of its row and so fetches chunk (l % 8)
+  // ^ swizzle.
   const uint8_t* from_a[4];
-  const uint8_t* from_b[4];
+  const uint8_t* from_b[2 * kNT];
   int chunk[2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int t = 32 * wave + 8 * q + (lane >> 3);
-    const int c = (lane & 7) ^ chunk_swizzle(t);
-    if (q < 2) chunk[q] = c;  // the swizzle repeats every 16 rows
-    from_a[q] = p.A + (int64_t)min(row0 + t, p.M - 1) * p.K + 16 * c;
-    from_b[q] = p.B + b_row(t) * p.K + 16 * c;
+  for (int q = 0; q < 2 * kNT; ++q) {
+    const int t = 8 * q + (lane >> 3);
+    const int c = (lane & 7) ^ chunk_swizzle(t);  // the swizzle repeats every 16 rows
+    if (q < 2) chunk[q] = c;
+    if (q < 4) from_a[q < 4 ? q : 0] = p.A + (int64_t)min(row0 + 32 * wave + t, p.M - 1) * p.K + 16 * c;
+    from_b[q] = p.B + b_row(16 * kNT * wave + t) * p.K + 16 * c;
+  }
+  // Scales: piece n of 64 rows, A's two and then B's.
+  const uint8_t* from_s[G::kScaleDmas];
+  int piece[G::kScaleDmas];
+#pragma unroll
+  for (int e = 0; e < G::kScaleDmas; ++e) {
+    int n = wave + 4 * e;
+    if (n >= 2 + kNT) n -= 2;  // two waves repeat the last two, the same bytes
+    piece[e] = n;
+    const int64_t at =
+        n < 2 ? (int64_t)min(row0 + 64 * n + lane, p.M - 1) * p.kblocks
+              : (b_row(64 * (n - 2) + lane) >> p.b_shift) * p.kblocks;
+    from_s[e] = static_cast<const uint8_t*>(n < 2 ? p.As : p.Bs) + (kF32Scale ? 4 : 1) * at;
   }
   const uint32_t lds0 = lds_addr(lds);
-  const int last_bytes = p.K - (p.kblocks - 1) * kFp8Block;
-  const auto load_step = [&](int kb, int slot) {
-    const uint32_t to_a = __builtin_amdgcn_readfirstlane(lds0 + slot * kSlotBytes + wave * 4096);
-    const uint32_t to_b = to_a + 2 * kSlotBytes;
-    const int64_t k = (int64_t)kb * kRowBytes;
-    const bool tail = kTail && kb == p.kblocks - 1;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint8_t* ga = from_a[q] + k;
-      const uint8_t* gb = from_b[q] + k;
-      if (tail && 16 * chunk[q & 1] >= last_bytes) ga = gb = kFp8Zeros;
-      dma16(ga, to_a + 1024 * q);
-      dma16(gb, to_b + 1024 * q);
+  const int last = p.kblocks - 1;
+  const int last_bytes = p.K - last * kFp8Block;
+  // DMA n of a step: A's four, B's 2 kNT, the scales'.
+  const auto load = [&](auto n, int k, uint32_t slot) {
+    constexpr int q = n() < 4 ? n() : n() - 4;
+    if constexpr (q < 2 * kNT) {
+      const int64_t at = (int64_t)k * kRowBytes;
+      const uint8_t* g = (n() < 4 ? from_a[q < 4 ? q : 0] : from_b[q]) + at;
+      if (kTail) g = 16 * chunk[q & 1] < (k == last ? last_bytes : kRowBytes) ? g : kFp8Zeros;
+      const uint32_t to = n() < 4 ? wave * 4096 : kRows * kRowBytes + wave * 2048 * kNT;
+      dma16(g, __builtin_amdgcn_readfirstlane(lds0 + slot + to) + 1024 * q);
+    } else {
+      constexpr int e = q - 2 * kNT;
+      const uint32_t to =
+          __builtin_amdgcn_readfirstlane(lds0 + slot + G::kTiles + 256 * piece[e]);
+      if constexpr (kF32Scale)
+        dma4(from_s[e] + (int64_t)4 * k, to);
+      else
+        dma1(from_s[e] + k, to);
     }
   };
+  const auto load_step = [&](int kb, uint32_t slot) {
+    for_each([&](auto n) { load(n, min(kb, last), slot); },
+             std::make_integer_sequence<int, G::kDmas>());
+  };
 
-  // Scales. UE8M0: words of four blocks per row of the lane's tiles; FP32: the
-  // next block's own.
-  const int m_wave = row0 + 64 * wy;
-  int64_t sa_at[2], sb_at[2];
+  const uint32_t x = (uint32_t)(h ^ chunk_swizzle(r));
+  const uint32_t frag_a = (uint32_t)(64 * wy + r) * kRowBytes;
+  const uint32_t frag_b = (uint32_t)(kRows + 32 * kNT * wx + r) * kRowBytes;
+  uint32_t at_a[4], at_b[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    sa_at[i] = (int64_t)min(m_wave + 32 * i + r, p.M - 1) * p.kblocks;
-    sb_at[i] = (b_row(64 * wx + 32 * i + (kF32Scale ? 0 : r)) >> p.b_shift) * p.kblocks;
+  for (int c = 0; c < 4; ++c) {
+    at_a[c] = frag_a + 16 * ((2 * c) ^ x);
+    at_b[c] = frag_b + 16 * ((2 * c) ^ x);
   }
-  const int64_t sa_total = (int64_t)p.M * p.kblocks;
-  const int64_t b_rows = kGlu ? 2 * (int64_t)p.N : p.N;
-  const int64_t sb_total = ((b_rows + (1 << p.b_shift) - 1) >> p.b_shift) * p.kblocks;
-  uint32_t sa[2], sb[2];
-  const auto load_scales = [&](int kb, uint32_t (&a)[2], uint32_t (&b)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (kF32Scale) {
-        a[i] = static_cast<const uint32_t*>(p.As)[sa_at[i] + kb];
-        b[i] = static_cast<const uint32_t*>(p.Bs)[sb_at[i] + kb];
-      } else {
-        a[i] = scale_word(static_cast<const uint8_t*>(p.As), sa_at[i] + kb, sa_total);
-        b[i] = scale_word(static_cast<const uint8_t*>(p.Bs), sb_at[i] + kb, sb_total);
-      }
+  // Read n of a step: scales, then the four chunks of B's tiles and of A's.
+  constexpr int kReads = 5 * (2 + kNT);
+  const auto read = [&](auto n, uint32_t slot, Frags<kNT>& f) {
+    const uint8_t* base = lds + slot;
+    if constexpr (n() < 2 + kNT) {
+      const uint32_t* s = reinterpret_cast<const uint32_t*>(base + G::kTiles);
+      if constexpr (n() < 2)
+        f.sa[n()] = s[64 * wy + 32 * n() + r];
+      else
+        f.sb[n() - 2] = s[kRows + 32 * kNT * wx + 32 * (n() - 2) + r];
+    } else {
+      constexpr int t = (n() - 2 - kNT) % (2 + kNT), c = (n() - 2 - kNT) / (2 + kNT);
+      if constexpr (t < kNT)
+        f.b[t].c[c] = *reinterpret_cast<const u32x4_t*>(base + at_b[c] + t * 32 * kRowBytes);
+      else
+        f.a[t - kNT].c[c] =
+            *reinterpret_cast<const u32x4_t*>(base + at_a[c] + (t - kNT) * 32 * kRowBytes);
     }
   };
 
-  v16_t acc[2][2];
+  v16_t acc[2][kNT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = v16_t{};
+    for (int j = 0; j < kNT; ++j) acc[i][j] = v16_t{};
 
-  const uint32_t x = (uint32_t)(h ^ chunk_swizzle(r));
-  const uint8_t* frag_a = lds + (64 * wy + r) * kRowBytes;
-  const uint8_t* frag_b = lds + 2 * kSlotBytes + (64 * wx + r) * kRowBytes;
-  const auto read = [&](const uint8_t* base, int slot, int tile, Frag& f) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      f.c[c] = *reinterpret_cast<const u32x4_t*>(base + slot * kSlotBytes + tile * 32 * kRowBytes +
-                                                 16 * ((2 * c) ^ x));
+  for (int s = 0; s < G::kSlots; ++s) load_step(s, s * G::kSlot);
+  wait_loads_and_meet<G::kDmas*(G::kSlots - 1)>();
+  uint32_t now = 0, next = G::kSlot;  // slots of steps kb and kb + 1
+  const auto step = [&](int kb, Frags<kNT>& f, Frags<kNT>& g) {
+    // Step kb + 1 has landed, in all waves, and step kb is in their registers.
+    wait_loads_and_meet<G::kDmas*(G::kSlots - 2)>();
+    const int k = min(kb + G::kSlots, last);  // past the last it is loaded again, and not used
+    multiply<kBf16, kF32Scale, kA, kNT>(acc, f, [&](auto n) {
+      constexpr int kPieces = kPiecesOf<kNT, kBf16>;
+      // The reads leave out the last piece, so that they have returned at the end.
+      constexpr int r0 = kReads * n() / (kPieces - 1), r1 = kReads * (n() + 1) / (kPieces - 1);
+      constexpr int d0 = G::kDmas * n() / kPieces, d1 = G::kDmas * (n() + 1) / kPieces;
+      if constexpr (n() < kPieces - 1)
+        for_each([&](auto m) { read(Int<r0 + m()>(), next, g); },
+                 std::make_integer_sequence<int, r1 - r0>());
+      for_each([&](auto m) { load(Int<d0 + m()>(), k, now); },
+               std::make_integer_sequence<int, d1 - d0>());
+    });
+    now = next;
+    next = next + G::kSlot == G::kSlots * G::kSlot ? 0 : next + G::kSlot;
   };
-
-  uint32_t na[2], nb[2];
-  load_scales(0, na, nb);
-  load_step(0, 0);
-  for (int kb = 0; kb < p.kblocks; ++kb) {
-    const int slot = kb & 1;
-    // Every load of this step has landed, in all waves, and the other slot has
-    // been read.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kF32Scale || (kb & 3) == 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        asm volatile("" : "+v"(na[i]), "+v"(nb[i]));
-        sa[i] = na[i];
-        sb[i] = nb[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sa[i] >>= 8;
-        sb[i] >>= 8;
-      }
-    }
-    if (kb + 1 < p.kblocks) {
-      if (kF32Scale || (kb & 3) == 3) load_scales(kb + 1, na, nb);
-      load_step(kb + 1, 1 - slot);
-    }
-    Frag a[2], b[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      read(frag_b, slot, i, b[i]);
-      read(frag_a, slot, i, a[i]);
-    }
-    if constexpr (kBf16) {
-      v16_t sums[2][2];
-      if constexpr (kF32Scale) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) sums[i][j] = v16_t{};
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          bf16x8_t a16[2], b16[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t alo = a[i].c[c][2 * e], ahi = a[i].c[c][2 * e + 1];
-            const uint32_t blo = b[i].c[c][2 * e], bhi = b[i].c[c][2 * e + 1];
-            a16[i] = fp8x8_to_bf16<kA>(alo, ahi, kF32Scale ? 1.0f : fp8_scale_value(sa[i] & 255));
-            b16[i] =
-                fp8x8_to_bf16<kE4M3>(blo, bhi, kF32Scale ? 1.0f : fp8_scale_value(sb[i] & 255));
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              v16_t& to = kF32Scale ? sums[i][j] : acc[i][j];
-              to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b16[j], a16[i], to, 0, 0, 0);
-            }
-        }
-      }
-      if constexpr (kF32Scale) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float f = __uint_as_float(sa[i]) * __uint_as_float(sb[j]);
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(f, sums[i][j][v], acc[i][j][v]);
-          }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if constexpr (kF32Scale) {
-            v16_t s = mfma_fp8_32<kA, 0>(b[j], a[i], 0, v16_t{}, 127, 127);
-            s = mfma_fp8_32<kA, 0>(b[j], a[i], 1, s, 127, 127);
-            const float f = __uint_as_float(sa[i]) * __uint_as_float(sb[j]);
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(f, s[v], acc[i][j][v]);
-          } else {
-            acc[i][j] = mfma_fp8_32<kA, 0>(b[j], a[i], 0, acc[i][j], sb[j], sa[i]);
-            acc[i][j] = mfma_fp8_32<kA, 0>(b[j], a[i], 1, acc[i][j], sb[j], sa[i]);
-          }
-        }
-    }
+  Frags<kNT> f, g;
+  for_each([&](auto n) { read(n, 0, f); }, std::make_integer_sequence<int, kReads>());
+  int kb = 0;
+  for (; kb + 2 <= p.kblocks; kb += 2) {
+    step(kb, f, g);
+    step(kb + 1, g, f);
   }
-  __syncthreads();
+  if (kb < p.kblocks) step(kb, f, g);
+  wait_loads_and_meet<0>();
 
   // Register 4 q + t of tile (i, j) holds row 32 i + r, column 32 j + 8 q + 4 h
   // + t of the wave's part. Each wave parks it in its own 16 KiB and stores
   // whole lines: FP32 rows of 64 columns as 256 bytes, 16-byte chunk c at c ^
   // (row % 16); BF16 rows of `width` columns as 128 bytes, chunk c at c ^ (row
   // % 8).
-  uint8_t* park = lds + wave * kSlotBytes;
+  uint8_t* park = lds + wave * 16384;
+  const int m_wave = row0 + 64 * wy;
   const int rows_left = p.M - m_wave;
   const auto store_bf16 = [&](uint16_t* to, int64_t ld, int cols, int width) {
     // to: the wave's first element; cols: how many columns there are
@@ -297,75 +375,85 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_fp8_kernel(Fp8GemmArgs p, in
         store_bf16(p.gu + (int64_t)m_wave * 2 * p.N + part * (int64_t)p.N + ncol,
                    2 * (int64_t)p.N, 32, 32);
     }
-  } else if constexpr (kOut == kFp8Bf16) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v16_t& v = acc[i][j];
-          park_bf16(32 * i + r, 32 * j + 8 * q + 4 * h, pack_bf16x2(v[4 * q], v[4 * q + 1]),
-                    pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
-        }
-    const int ncol = col0 + 64 * wx;
-    store_bf16(static_cast<uint16_t*>(p.C) + (int64_t)m_wave * p.N + ncol, p.N, p.N - ncol, 64);
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int part = 0; part < kNT / 2; ++part) {
+      const int ncol = col0 + 32 * kNT * wx + 64 * part, cols = p.N - ncol;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v16_t& v = acc[i][j];
-          const int c = 8 * j + 2 * q + h, row = 32 * i + r;
-          *reinterpret_cast<float4*>(park + row * 256 + 16 * (c ^ (row & 15))) =
-              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v16_t& v = acc[i][2 * part + j];
+            const int c = 8 * j + 2 * q + h, row = 32 * i + r;
+            if constexpr (kOut == kFp8Bf16)
+              park_bf16(row, 4 * c, pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                        pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+            else
+              *reinterpret_cast<float4*>(park + row * 256 + 16 * (c ^ (row & 15))) =
+                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+      if constexpr (kOut == kFp8Bf16) {
+        store_bf16(static_cast<uint16_t*>(p.C) + (int64_t)m_wave * p.N + ncol, p.N, cols, 64);
+      } else {
+        float* to = static_cast<float*>(p.C) + (int64_t)m_wave * p.N + ncol;
+        if (p.N % 4 == 0) {
+          for (int x0 = 0; x0 < 64; x0 += 4) {
+            const int row = x0 + (lane >> 4), c = lane & 15;
+            const float4 v =
+                *reinterpret_cast<const float4*>(park + row * 256 + 16 * (c ^ (row & 15)));
+            if (row < rows_left && 4 * c < cols)
+              *reinterpret_cast<float4*>(to + (int64_t)row * p.N + 4 * c) = v;
+          }
+        } else {
+          for (int row = 0; row < min(64, rows_left); ++row) {
+            const float v = *reinterpret_cast<const float*>(
+                park + row * 256 + 16 * ((lane >> 2) ^ (row & 15)) + 4 * (lane & 3));
+            if (lane < cols) to[(int64_t)row * p.N + lane] = v;
+          }
         }
-    const int ncol = col0 + 64 * wx, cols = p.N - ncol;
-    float* to = static_cast<float*>(p.C) + (int64_t)m_wave * p.N + ncol;
-    if (p.N % 4 == 0) {
-      for (int x0 = 0; x0 < 64; x0 += 4) {
-        const int row = x0 + (lane >> 4), c = lane & 15;
-        const float4 v = *reinterpret_cast<const float4*>(park + row * 256 + 16 * (c ^ (row & 15)));
-        if (row < rows_left && 4 * c < cols)
-          *reinterpret_cast<float4*>(to + (int64_t)row * p.N + 4 * c) = v;
-      }
-    } else {
-      for (int row = 0; row < min(64, rows_left); ++row) {
-        const float v = *reinterpret_cast<const float*>(
-            park + row * 256 + 16 * ((lane >> 2) ^ (row & 15)) + 4 * (lane & 3));
-        if (lane < cols) to[(int64_t)row * p.N + lane] = v;
       }
     }
   }
 }
 
-template <bool kBf16, bool kF32Scale, Fp8Out kOut, Fp8Type kA>
+template <int kNT, bool kBf16, bool kF32Scale, Fp8Out kOut, Fp8Type kA>
 hipError_t launch(const Fp8GemmArgs& a, hipStream_t stream) {
-  constexpr int kCols = kOut == kFp8Glu ? kTile / 2 : kTile;
-  const int64_t tiles_m = ((int64_t)a.M + kTile - 1) / kTile;
+  constexpr int kCols = kOut == kFp8Glu ? Geom<kNT>::kCols / 2 : Geom<kNT>::kCols;
+  const int64_t tiles_m = ((int64_t)a.M + kRows - 1) / kRows;
   const int64_t tiles_n = ((int64_t)a.N + kCols - 1) / kCols;
   const dim3 grid = grid_of(tiles_m * tiles_n, kThreads);
   if (a.K % kFp8Block != 0)
-    hipLaunchKernelGGL((gemm_fp8_kernel<kBf16, kF32Scale, kOut, kA, true>), grid, dim3(kThreads),
-                       0, stream, a, (int)tiles_m, (int)tiles_n);
+    hipLaunchKernelGGL((gemm_fp8_kernel<kNT, kBf16, kF32Scale, kOut, kA, true>), grid,
+                       dim3(kThreads), 0, stream, a, (int)tiles_m, (int)tiles_n);
   else
-    hipLaunchKernelGGL((gemm_fp8_kernel<kBf16, kF32Scale, kOut, kA, false>), grid, dim3(kThreads),
-                       0, stream, a, (int)tiles_m, (int)tiles_n);
+    hipLaunchKernelGGL((gemm_fp8_kernel<kNT, kBf16, kF32Scale, kOut, kA, false>), grid,
+                       dim3(kThreads), 0, stream, a, (int)tiles_m, (int)tiles_n);
   return hipGetLastError();
+}
+
+template <bool kBf16, bool kF32Scale, Fp8Out kOut, Fp8Type kA>
+hipError_t launch_sized(const Fp8GemmArgs& a, hipStream_t stream) {
+  // Wide tiles read less of A and B for a product, where they still fill the chip.
+  const int64_t wide = ((int64_t)a.M + 127) / 128 * (((int64_t)a.N + 255) / 256);
+  if constexpr (kBf16 && kF32Scale)  // the registers do not do for 128 x 256
+    return launch<2, kBf16, kF32Scale, kOut, kA>(a, stream);
+  else
+    return wide >= 256 ? launch<4, kBf16, kF32Scale, kOut, kA>(a, stream)
+                     : launch<2, kBf16, kF32Scale, kOut, kA>(a, stream);
 }
 
 template <Fp8Type kA>
 hipError_t launch_typed(const Fp8GemmArgs& a, Fp8Out out, bool f32, hipStream_t stream) {
   if (out == kFp8F32)
-    return f32 ? launch<true, true, kFp8F32, kA>(a, stream)
-               : launch<true, false, kFp8F32, kA>(a, stream);
-  return f32 ? launch<false, true, kFp8Bf16, kA>(a, stream)
-             : launch<false, false, kFp8Bf16, kA>(a, stream);
+    return f32 ? launch_sized<true, true, kFp8F32, kA>(a, stream)
+               : launch_sized<true, false, kFp8F32, kA>(a, stream);
+  return f32 ? launch_sized<false, true, kFp8Bf16, kA>(a, stream)
+             : launch<2, false, false, kFp8Bf16, kA>(a, stream);
 }
 
-constexpr int kSmallMaxM = 512;
+constexpr int kSmallMaxM = 64;
 
 // Whether a product runs on 256 x 256 tiles: where they fill the chip.
 bool big_tiles(int64_t M, int64_t N) {
@@ -396,7 +484,7 @@ hipError_t launch_gemm_fp8_swiglu(const Fp8GemmArgs& a, uint8_t* codes, uint8_t*
   if (!g.C) g.C = workspace;
   const hipError_t e = a.M <= kSmallMaxM || fp8_short_scales(a.M, 2 * (int64_t)a.N, a.kblocks, 7)
                            ? launch_gemm_fp8_small(g, kFp8Glu, kE4M3, false, stream)
-                           : launch<false, false, kFp8Glu, kE4M3>(g, stream);
+                           : launch<2, false, false, kFp8Glu, kE4M3>(g, stream);
   if (e != hipSuccess) return e;
   Fp8QuantArgs q{};
   q.x = static_cast<const uint16_t*>(g.C);

@@ -311,7 +311,7 @@ void gemm_fp8_tile_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, Fp8ActOut act
     if (q < 2) c.chunk[q] = chunk;
     const uint32_t from = 16 * chunk + kBias - (q % 4) * 1024;
     c.off_a[q] = (uint32_t)(min(row0 + t, p.M - 1) - (int)a_first) * (uint32_t)p.K + from;
-    // Up's rows lie I rows behind gate's: within 32 bits (launch_gemm_fp8_tile).
+    // Up's rows lie I rows behind gate's: within 32 bits (gemm_fp8_swiglu_small).
     c.off_b[q] = (uint32_t)(b_row(t) - b_first) * (uint32_t)p.K + from;
   }
   const uint32_t x = (uint32_t)(h ^ chunk_swizzle(r)) << 4;

@@ -7,66 +7,95 @@
 // dgu^T, the operand of dW13 = dgu^T x). Neither gradient is written in BF16.
 //
 // Bound by memory: 6 bytes read and 2 (1 + 1/128) x 2 written per element of
-// act. One workgroup of 512 threads holds a 128 x 128 tile of act, thread
-// (g, c) rows 4 g .. + 3 of columns 8 c .. + 7 of both gradients in registers
-// (64 values), so a row's block is 16 lanes (four DPP moves) and a column's
-// the 32 groups g: two shuffles, then a maximum in LDS. The transposed codes
-// go through LDS, so that all codes leave as whole 128-byte lines.
+// act; the VALU's share is near it, so magnitudes are compared as floats, two in
+// one v_max3. One workgroup of 1024 threads holds a 128 x 128 tile of act, thread
+// (g, c) rows 4 g .. + 3 of columns 4 c .. + 3 of both gradients in registers (32
+// values, four waves a SIMD: 16384 x 14336 608 us, 3.9 TB/s; with 64 values in 512
+// threads it was two waves, 667 us; with eight waves, whose registers spill, 597,
+// but 4096 x 4096 50 instead of 45). A row's block is 32 lanes (DPP moves and one swap
+// of lanes), a column's the 32 groups g: one swap, which also puts two columns
+// into one register, then a maximum in LDS. The transposed codes go through LDS,
+// so that all codes leave as whole 128-byte lines.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "fp8.h"
 
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kTile = kFp8Block;
-constexpr int kRows = 4;           // of a thread
+constexpr int kPatch = 4;          // rows and columns of a thread
 constexpr int kMaxGrid = 1 << 20;  // workgroups; the kernel strides over the rest
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// |v| as an integer that orders like it; 0 for infinities and NaN.
-__device__ __forceinline__ int finite_abs(float v) {
-  const int b = (int)(__float_as_uint(v) & 0x7FFFFFFFu);
-  return b < 0x7F800000 ? b : 0;
+__device__ __forceinline__ uint2 load_once(const uint16_t* x) {
+  typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+  const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(x));
+  return make_uint2(v[0], v[1]);
+}
+
+// |v|; 0 for infinities and NaN where kFinite (a maximum passes over NaN).
+template <bool kFinite>
+__device__ __forceinline__ float magnitude(float v) {
+  const float m = __builtin_fabsf(v);
+  return kFinite && !(m < __builtin_inff()) ? 0.0f : m;
+}
+
+// Maxima of two values over pairs of half waves: a's in the lower half, b's in
+// the upper one.
+__device__ __forceinline__ float merge32_max(float a, float b) {
+  const auto s =
+      __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __builtin_fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+// Maximum over the 32 lanes of a half wave.
+__device__ __forceinline__ float half_max(float v) {
+  const uint32_t m = (uint32_t)row16_max((int)__float_as_uint(v));  // not negative: orders as int
+  const auto s = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  return __builtin_fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
 
 template <Fp8Type kType>
-__global__ __launch_bounds__(kThreads) void swiglu_fp8_backward_kernel(SwigluBackwardArgs p,
-                                                                       int mblocks, int iblocks) {
+__global__ __launch_bounds__(kThreads, 4) void swiglu_fp8_backward_kernel(SwigluBackwardArgs p,
+                                                                          int mblocks,
+                                                                          int iblocks) {
   __shared__ __align__(16) uint8_t turned[2][kTile * kTile];
   __shared__ __align__(16) int tops[2][kTile];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int c = tid & 15, g = tid >> 4;
+  const int c = tid & 31, g = tid >> 5;
   const int64_t Mp = ((int64_t)p.M + 15) / 16 * 16;
   const int64_t tiles = (int64_t)mblocks * iblocks;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int mb = (int)(t / iblocks), ib = (int)(t - (int64_t)mb * iblocks);
-    const int64_t m0 = (int64_t)mb * kTile + kRows * g;
-    const int i0 = ib * kTile + 8 * c;
+    const int64_t m0 = (int64_t)mb * kTile + kPatch * g;
+    const int i0 = ib * kTile + kPatch * c;
     if (tid < 2 * kTile) (&tops[0][0])[tid] = 0;
 
-    u32x4_t vd[kRows], vg[kRows], vu[kRows];
+    uint2 vd[kPatch], vg[kPatch], vu[kPatch];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      vd[i] = vg[i] = vu[i] = u32x4_t{};
+    for (int i = 0; i < kPatch; ++i) {
+      vd[i] = vg[i] = vu[i] = make_uint2(0, 0);
       if (m0 + i < p.M) {
         const uint16_t* gu = p.gu + (m0 + i) * 2 * p.I + i0;
-        vd[i] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4_t*>(p.dact + (m0 + i) * p.I + i0));
-        vg[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(gu));
-        vu[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(gu + p.I));
+        vd[i] = load_once(p.dact + (m0 + i) * p.I + i0);
+        vg[i] = load_once(gu);
+        vu[i] = load_once(gu + p.I);
       }
     }
-    float d[2][kRows][8];  // dg, du
+    float d[2][kPatch][kPatch];  // dg, du
+    float most = 0;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+    for (int i = 0; i < kPatch; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t wd = vd[i][j / 2], wg = vg[i][j / 2], wu = vu[i][j / 2];
+      for (int j = 0; j < kPatch; ++j) {
+        const uint32_t wd = j < 2 ? vd[i].x : vd[i].y, wg = j < 2 ? vg[i].x : vg[i].y;
+        const uint32_t wu = j < 2 ? vu[i].x : vu[i].y;
         const float dy = j & 1 ? bf16_hi(wd) : bf16_lo(wd);
         const float gg = j & 1 ? bf16_hi(wg) : bf16_lo(wg);
         const float uu = j & 1 ? bf16_hi(wu) : bf16_lo(wu);
@@ -74,63 +103,79 @@ __global__ __launch_bounds__(kThreads) void swiglu_fp8_backward_kernel(SwigluBac
         const float ds = dy * s;
         d[0][i][j] = ds * uu * fmaf(gg, 1.0f - s, 1.0f);
         d[1][i][j] = ds * gg;
+        most = __builtin_fmaxf(__builtin_fmaxf(most, __builtin_fabsf(d[0][i][j])),
+                               __builtin_fabsf(d[1][i][j]));
       }
-    __syncthreads();  // tops is clear, and the last tile's turned has been read
+    float row_top[2][kPatch];
+    const auto find_tops = [&](auto finite) {
+      constexpr bool kFinite = decltype(finite)::value;
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < 2; ++w) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        int top = 0;
+        for (int j = 0; j < kPatch; j += 2) {
+          float col[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) top = max(top, finite_abs(d[w][i][j]));
-        top = max(top, __shfl_xor(top, 16));
-        top = max(top, __shfl_xor(top, 32));
-        if (lane < 16) atomicMax(&tops[w][8 * c + j], top);
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < kPatch; ++i)
+              col[e] = __builtin_fmaxf(col[e], magnitude<kFinite>(d[w][i][j + e]));
+          atomicMax(&tops[w][kPatch * c + j + (lane >> 5)],
+                    (int)__float_as_uint(merge32_max(col[0], col[1])));
+        }
+#pragma unroll
+        for (int i = 0; i < kPatch; ++i) {
+          float row = 0;
+#pragma unroll
+          for (int j = 0; j < kPatch; ++j)
+            row = __builtin_fmaxf(row, magnitude<kFinite>(d[w][i][j]));
+          row_top[w][i] = half_max(row);
+        }
       }
+    };
+    // tops is clear, and the last tile's turned has been read. Infinities are
+    // rare, so leaving them out of the maxima is a path of its own.
+    if (__syncthreads_or(!(most < __builtin_inff())))
+      find_tops(std::true_type());
+    else
+      find_tops(std::false_type());
     // Rows.
     const int64_t kblocks = 2 * (int64_t)iblocks;
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        int top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, finite_abs(d[w][i][j]));
-        const uint32_t byte = fp8_scale_byte_f32<kType>((uint32_t)row16_max(top));
+      for (int i = 0; i < kPatch; ++i) {
+        const uint32_t byte = fp8_scale_byte_f32<kType>(__float_as_uint(row_top[w][i]));
         const float s = fp8_scale_value(byte);
         const float* v = d[w][i];
-        uint2 code;
-        code.x = fp8_pair_f32<kType, true>(fp8_pair_f32<kType, false>(0, v[0], v[1], s), v[2],
-                                           v[3], s);
-        code.y = fp8_pair_f32<kType, true>(fp8_pair_f32<kType, false>(0, v[4], v[5], s), v[6],
-                                           v[7], s);
+        const uint32_t code =
+            fp8_pair_f32<kType, true>(fp8_pair_f32<kType, false>(0, v[0], v[1], s), v[2], v[3], s);
         if (m0 + i < p.M) {
-          *reinterpret_cast<uint2*>(p.codes + (m0 + i) * 2 * p.I + (int64_t)w * p.I + i0) = code;
+          *reinterpret_cast<uint32_t*>(p.codes + (m0 + i) * 2 * p.I + (int64_t)w * p.I + i0) =
+              code;
           if (c == 0) p.scales[(m0 + i) * kblocks + w * iblocks + ib] = (uint8_t)byte;
         }
       }
     __syncthreads();  // tops is whole
-    // Columns: column 8 c + j's 4 bytes of group g at dword g ^ 4 (c % 8) of
-    // its 128-byte row, so that the lanes of one store fall on all banks.
+    // Columns: column 4 c + j's 4 bytes of group g at dword g ^ c of its 128-byte
+    // row, so that the lanes of one store fall on all banks.
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t byte = fp8_scale_byte_f32<kType>((uint32_t)tops[w][8 * c + j]);
+      for (int j = 0; j < kPatch; ++j) {
+        const uint32_t byte = fp8_scale_byte_f32<kType>((uint32_t)tops[w][kPatch * c + j]);
         const float s = fp8_scale_value(byte);
-        const uint32_t code = fp8_pair_f32<kType, true>(
-            fp8_pair_f32<kType, false>(0, d[w][0][j], d[w][1][j], s), d[w][2][j], d[w][3][j], s);
-        *reinterpret_cast<uint32_t*>(turned[w] + (8 * c + j) * kTile + 4 * (g ^ (4 * (c & 7)))) =
-            code;
-        if (g == 0)
-          p.scales_t[((int64_t)w * p.I + i0 + j) * mblocks + mb] = (uint8_t)byte;
+        *reinterpret_cast<uint32_t*>(turned[w] + (kPatch * c + j) * kTile + 4 * (g ^ c)) =
+            fp8_pair_f32<kType, true>(fp8_pair_f32<kType, false>(0, d[w][0][j], d[w][1][j], s),
+                                      d[w][2][j], d[w][3][j], s);
+        if (g == 0) p.scales_t[((int64_t)w * p.I + i0 + j) * mblocks + mb] = (uint8_t)byte;
       }
     __syncthreads();  // turned is whole
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int w = it >> 1, col = 64 * (it & 1) + (tid >> 3), q = tid & 7;
-      const uint4 v =
-          *reinterpret_cast<const uint4*>(turned[w] + col * kTile + 16 * (q ^ ((col >> 3) & 7)));
+    for (int w = 0; w < 2; ++w) {
+      const int col = tid >> 3, q = tid & 7, x = col / kPatch;
+      uint4 v = *reinterpret_cast<const uint4*>(turned[w] + col * kTile + 16 * (q ^ (x >> 2)));
+      if (x & 1) v = make_uint4(v.y, v.x, v.w, v.z);
+      if (x & 2) v = make_uint4(v.z, v.w, v.x, v.y);
       const int64_t mm = (int64_t)mb * kTile + 16 * q;
       if (mm < Mp)
         *reinterpret_cast<uint4*>(p.codes_t + ((int64_t)w * p.I + ib * kTile + col) * Mp + mm) = v;

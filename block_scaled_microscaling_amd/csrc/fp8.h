@@ -1,5 +1,5 @@
-// Shared by the FP8 kernels (quantize_fp8.hip, gemm_fp8.hip,
-// gemm_fp8_small.hip, swiglu_fp8.hip): the scale rule, conversions, the
+// Shared by the FP8 kernels (quantize_fp8.hip, gemm_fp8.hip, gemm_fp8_small.hip,
+// gemm_fp8_tile.hip, swiglu_fp8.hip): the scale rule, conversions, the
 // matrix instructions and the launchers that api_fp8.hip calls.
 //
 // An FP8 operand is E4M3 or E5M2 codes with one scale per block of 128

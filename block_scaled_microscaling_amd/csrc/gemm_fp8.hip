@@ -213,7 +213,8 @@ void gemm_fp8_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n) {
     const int t = 8 * q + (lane >> 3);
     const int c = (lane & 7) ^ chunk_swizzle(t);  // the swizzle repeats every 16 rows
     if (q < 2) chunk[q] = c;
-    if (q < 4) from_a[q < 4 ? q : 0] = p.A + (int64_t)min(row0 + 32 * wave + t, p.M - 1) * p.K + 16 * c;
+    if (q < 4)
+      from_a[q < 4 ? q : 0] = p.A + (int64_t)min(row0 + 32 * wave + t, p.M - 1) * p.K + 16 * c;
     from_b[q] = p.B + b_row(16 * kNT * wave + t) * p.K + 16 * c;
   }
   // Scales: piece n of 64 rows, A's two and then B's.
@@ -435,7 +436,9 @@ hipError_t launch(const Fp8GemmArgs& a, hipStream_t stream) {
 
 template <bool kBf16, bool kF32Scale, Fp8Out kOut, Fp8Type kA>
 hipError_t launch_sized(const Fp8GemmArgs& a, hipStream_t stream) {
-  // Wide tiles read less of A and B for a product, where they still fill the chip.
+  // Wide tiles read less of A and B for a product, where they still fill the chip
+  // (FP32 scales: 16384 x 4096 x 14336 1145 against 1331 us, 2048 x 4096 x 4096, 256
+  // of them, 47 against 55; 2048 x 2048 x 2048, half of that, 23.6 against 15.6).
   const int64_t wide = ((int64_t)a.M + 127) / 128 * (((int64_t)a.N + 255) / 256);
   if constexpr (kBf16 && kF32Scale)  // the registers do not do for 128 x 256
     return launch<2, kBf16, kF32Scale, kOut, kA>(a, stream);
@@ -457,12 +460,15 @@ int64_t tiles(int64_t M, int64_t N, int64_t side) {
   return (M + side - 1) / side * ((N + side - 1) / side);
 }
 
-// The kernel of a product whose operands the matrix instructions bound.
-// Few rows, or few tiles of a long K: the one that splits K over its waves (128
-// x 4096 x 4096 12.6 against 15.2 us here, 96 x 8192 x 8192 FP32 37.6 against
-// 48.2; but 512 x 2048 x 2048 11.9 against 9.5, 128 x 28672 x 4096 58 against 34).
+// Whether a product goes to the kernel that splits K over its waves: few rows; few
+// tiles of a long K (128 x 8192 x 4096 16.8 us there, 128 x 4096 x 4096 10.6 against
+// 15.2 here; but 128 x 28672 x 4096 58 against 34); or at most 512 tiles of 32 x 16, two
+// a CU, whatever K (128 x 2048 x 2048 7.4 us there, 9.3 here, FP32 results 7.2 and
+// 15.2; 512 x 512 x 512 5.0 and 5.3, x 1024 6.9 and 6.6; but 512 x 2048 x 2048, past
+// that, 11.9 against 9.5).
 bool few_tiles(int64_t M, int64_t N, int64_t kblocks) {
-  return M <= 64 || (tiles(M, N, 128) <= 64 && kblocks >= 32);
+  return M <= 64 || (M + 31) / 32 * ((N + 15) / 16) <= 512 ||
+         (tiles(M, N, 128) <= 64 && kblocks >= 32);
 }
 // 256 x 256 tiles where they fill half the chip, which is two rounds of tiles
 // here (1024 x 8192 x 8192 82 against 91 us; 1024 x 4096 x 4096 41 against 19).

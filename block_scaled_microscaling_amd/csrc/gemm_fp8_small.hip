@@ -24,9 +24,9 @@
 //
 // Arithmetic. The codes go to BF16, exact, and through v_mfma_f32_16x16x32
 // (fp8.h): memory bounds products of few rows, so the accuracy costs nothing.
-// With more than 64 rows, where it no longer does, BF16 results take the FP8
-// v_mfma_scale_f32_16x16x128 (kBf16 false). UE8M0 scales are applied in the conversion or the
-// instruction; FP32 scales multiply each block's sums: acc += (sa sb) * sums,
+// On 64 x 64 tiles, where it no longer does, BF16 results take the FP8
+// v_mfma_scale_f32_16x16x128 (kBf16 false). UE8M0 scales are applied in the
+// conversion or the instruction; FP32 scales multiply each block's sums: acc += (sa sb) * sums,
 // B's scale the same for all of the tile's rows.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -98,8 +98,8 @@ constexpr int kWavesOf = kMT + kNB <= 4 ? 4 : 2;
 // kShort: a scale array of fewer than four bytes, which are loaded one by one.
 template <int kMT, int kNT, Fp8Out kOut, Fp8Type kA, bool kF32Scale, bool kBf16, bool kStream,
           bool kShort>
-__global__ __launch_bounds__(kThreads, (kWavesOf<kMT, (kOut == kFp8Glu ? 2 * kNT : kNT)>)) void gemm_fp8_small_kernel(Fp8GemmArgs p, int tiles_m,
-                                                                  int tiles_n, int run) {
+__global__ __launch_bounds__(kThreads, (kWavesOf<kMT, (kOut == kFp8Glu ? 2 * kNT : kNT)>))
+void gemm_fp8_small_kernel(Fp8GemmArgs p, int tiles_m, int tiles_n, int run) {
   constexpr bool kGlu = kOut == kFp8Glu;
   constexpr int kNB = kGlu ? 2 * kNT : kNT;
   // A wave's rows on their way into fragments; its sums at the end.
@@ -377,14 +377,26 @@ hipError_t launch(const Fp8GemmArgs& a, hipStream_t stream) {
 
 template <Fp8Out kOut, Fp8Type kA, bool kF32Scale>
 hipError_t launch_sized(const Fp8GemmArgs& a, hipStream_t stream) {
-  constexpr int kTwo = kOut == kFp8Glu ? 1 : 2;  // gate and up tiles come in pairs
+  constexpr int kPair = kOut == kFp8Glu ? 2 : 1;  // gate and up tiles come in pairs
+  constexpr int kTwo = 2 / kPair;
   if constexpr (!kF32Scale) {
     if (fp8_short_scales(a.M, kOut == kFp8Glu ? 2 * (int64_t)a.N : a.N, a.kblocks, a.b_shift))
       return launch<1, 1, kOut, kA, kF32Scale, true, true>(a, stream);
   }
+  // One tile of rows where it holds all of A. More rows: the tile that reads A and
+  // B least among those that leave no CU without a workgroup: 32 x 16 up to two
+  // workgroups a CU (64 x 2048 x 4096 5.8 us against 11.4 with 64 x 32; 64 x 8192 x
+  // 2048, past that, 12.3 against 9.7), 64 x 32 up to one (256 x 2048 x 4096 10.3
+  // against 12.5 with 64 x 64; 256 x 4096 x 4096, past that, 18.9 against 13.0), or
+  // two where 64 x 64 would be on BF16 instructions too (96 x 8192 x 8192 FP32 33.4
+  // against 37.9). A tile of gate+up has twice the rows of B, so half as many do (64 x
+  // 4096 x 2048 12.7 against 15.3; 64 x 4096 x 4096, past that, 22.8 against 16.7).
+  const auto tiles = [&](int64_t m, int64_t n) { return (a.M + m - 1) / m * ((a.N + n - 1) / n); };
   if (a.M <= 16) return launch<1, 1, kOut, kA, kF32Scale>(a, stream);
-  if (a.M <= 32) return launch<2, 1, kOut, kA, kF32Scale>(a, stream);
-  if (a.M <= 64) return launch<4, kTwo, kOut, kA, kF32Scale>(a, stream);
+  if (a.M <= 32 || tiles(32, 16) <= 512 / kPair)
+    return launch<2, 1, kOut, kA, kF32Scale>(a, stream);
+  if (a.M <= 64 || tiles(64, 16 * kTwo) <= (kOut == kFp8F32 ? 512 : 256 / kPair))
+    return launch<4, kTwo, kOut, kA, kF32Scale>(a, stream);
   return launch<4, 2 * kTwo, kOut, kA, kF32Scale, kOut == kFp8F32>(a, stream);
 }
 

@@ -23,6 +23,12 @@
 // the waves meet: the step has been read, the next one's tiles have landed, and
 // the DMAs of the step after next go out beside the instructions, A's a whole
 // step ahead, B's, which have a third slot, one and a half.
+//
+// Measured: 8192^3 395 us (2.78 PFLOP/s; 128 x 128 tiles 643, one set of fragments
+// and two slots 425, three slots of B 397 before the K rotation below), 16384 x
+// 4096 x 14336 675, gate+up 16384 x 4096 x 14336 with g and u 1582. The
+// instructions alone run at 3.67 PFLOP/s, where power ends them; the tiles come
+// from L2 at 11 TB/s, which neither more DMAs under way nor other orders moved.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -6,7 +6,9 @@
 // input gradient's products contract over.
 //
 // All of them are bound by memory: 2 bytes read and 1 + 1/128 written per
-// element and form.
+// element and form (8192 x 8192 both ways 50.7 us, 5.3 TB/s; 28672 x 4096 in
+// 128 x 128 blocks both ways 93 us, 5.1 TB/s, a large copy's rate; 1 x 4096
+// 2 us beside a launch).
 //
 // Rows alone (quantize_fp8_rows_kernel): 16 lanes hold one block, 16 bytes (8
 // values) each, so a wave reads 4 blocks, 1 KiB, and its codes leave as whole
@@ -218,7 +220,8 @@ hipError_t launch(const Fp8QuantArgs& a, int block_rows, hipStream_t stream) {
 
 hipError_t launch_quantize_fp8(const Fp8QuantArgs& a, int block_rows, Fp8Type type,
                                hipStream_t stream) {
-  return type == kE4M3 ? launch<kE4M3>(a, block_rows, stream) : launch<kE5M2>(a, block_rows, stream);
+  return type == kE4M3 ? launch<kE4M3>(a, block_rows, stream)
+                       : launch<kE5M2>(a, block_rows, stream);
 }
 
 }  // namespace mxfp4

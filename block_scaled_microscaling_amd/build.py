@@ -49,7 +49,7 @@ def build(verbose=True):
     return LIB
 
 
-# The tensor layer of the few-token operators (csrc/tensors.cpp): a Python
+# The tensor layer of the few-token and FP8 operators (csrc/tensors.cpp): a Python
 # extension against the installed torch, built next to the library by g++.
 TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
 TENSORS_LIB = os.path.join(HERE, "_tensors.so")

@@ -760,7 +760,9 @@ def gemm_fp8(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=None):
     only, [N, ceil(K/128)]. Scales are uint8 (UE8M0) or float32, both alike;
     any M and N, K % 16 == 0.
 
-    out_dtype: torch.bfloat16 (default) or torch.float32.
+    out_dtype: torch.bfloat16 (default) or torch.float32. FP32 results add exact
+    products; large BF16 ones use the FP8 matrix instructions, which are off by
+    1.3e-5 of a typical sum before its rounding to BF16.
     """
     y = (_ext or load_tensors()).gemm_fp8(a, a_scales, b, b_scales, out_dtype, out, stream)
     if type(y) is int:

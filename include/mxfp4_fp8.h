@@ -57,7 +57,11 @@ int mxfp4_quantize_fp8_2d(const void* x_bf16, int64_t ldx, int64_t M, int64_t K,
                           int64_t block_rows, int code_type, int scale_type, void* codes,
                           void* scales, void* codes_t, void* scales_t, void* stream);
 
-/* C[m, n] = sum_k dq(A[m, k]) dq(B[n, k]), FP32 sums.
+/* C[m, n] = sum_k dq(A[m, k]) dq(B[n, k]), FP32 sums. FP32 results add exact
+ * products. BF16 results of large products use the FP8 matrix instructions,
+ * which cut eight neighbouring products off 2^-14 below the largest of them:
+ * each eight may be off by 2^-10 of their max |a| max |b|, a typical sum by
+ * 1.3e-5 of itself, before the rounding to BF16.
  * A_codes [M, K] of A_type, A_scales [M, ceil(K/128)]
  * B_codes [N, K] E4M3, B_scales [ceil(N/128), ceil(K/128)] (B_block_rows 128)
  *   or [N, ceil(K/128)] (B_block_rows 1, with UE8M0 scales only)
